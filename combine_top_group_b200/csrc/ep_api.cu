@@ -149,6 +149,14 @@ ep_status_t check_buf(const ep_buffer_t* b) {
 
 namespace ep {
 void set_last_error(const char* msg) { snprintf(g_msg, sizeof g_msg, "%s", msg); }
+
+ep_status_t fail(ep_status_t st, const char* fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_msg, sizeof g_msg, fmt, ap);
+    va_end(ap);
+    return st;
+}
 }  // namespace ep
 
 extern "C" {

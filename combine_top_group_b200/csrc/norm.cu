@@ -1,0 +1,411 @@
+// ep_rmsnorm and ep_rmsnorm_backward: residual addition, RMS norm and the
+// e4m3 cast in one pass over the row, and the gradient.
+//
+// Both are bound by HBM. The row stays in registers between the reduction and
+// the outputs, so each input is read once and each output written once.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "ep.h"
+#include "internal.h"
+
+namespace ep {
+namespace {
+
+// A thread holds VPT vectors of 16 channels; `tpr` threads (whole warps) hold
+// a row, and a CTA holds blockDim.x / tpr rows. Vector j of thread t covers
+// channels 16 * (t + j * tpr) .. +15, so 8 neighbouring lanes hold one
+// 128-channel scale block.
+constexpr int kVec = 16;
+
+struct NormParams {
+    int64_t N;
+    int H, nv, tpr;
+    const uint16_t* x;
+    const uint16_t* res;
+    const void* gamma;
+    int gamma_fp32;
+    float eps, inv_h;
+    uint16_t* h;
+    uint16_t* y;
+    uint8_t* q;
+    float* q_scale;
+    float* rstd;
+};
+
+__device__ __forceinline__ u32x8 ld256(const void* p) {
+    u32x8 a;
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(a.v[0]), "=r"(a.v[1]), "=r"(a.v[2]), "=r"(a.v[3]), "=r"(a.v[4]), "=r"(a.v[5]),
+                   "=r"(a.v[6]), "=r"(a.v[7])
+                 : "l"(p));
+    return a;
+}
+
+__device__ __forceinline__ void load_gamma(const void* gamma, int fp32, int c, float* g) {
+    if (fp32) {
+        const u32x8 a = ld256(static_cast<const float*>(gamma) + c);
+        const u32x8 b = ld256(static_cast<const float*>(gamma) + c + 8);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            g[i] = __uint_as_float(a.v[i]);
+            g[8 + i] = __uint_as_float(b.v[i]);
+        }
+    } else {
+        const u32x8 a = ld256(static_cast<const uint16_t*>(gamma) + c);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            g[2 * i] = bf16lo(a.v[i]);
+            g[2 * i + 1] = bf16hi(a.v[i]);
+        }
+    }
+}
+
+// Sum over the tpr threads of the caller's row, the same bits in each. red
+// holds 32 floats. Every thread of the CTA calls it.
+__device__ __forceinline__ float row_sum(float v, int tpr, float* red) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
+    if (tpr == 32) return v;
+    const int warp = threadIdx.x >> 5, wpr = tpr >> 5, first = warp / wpr * wpr;
+    if ((threadIdx.x & 31) == 0) red[warp] = v;
+    __syncthreads();
+    float s = 0.f;
+    for (int w = 0; w < wpr; ++w) s += red[first + w];
+    return s;
+}
+
+template <int VPT>
+__global__ void __launch_bounds__(1024) rmsnorm_kernel(NormParams p) {
+    __shared__ float red[32];
+    const int rpc = blockDim.x / p.tpr;
+    const int sub = threadIdx.x / p.tpr, t = threadIdx.x - sub * p.tpr;
+    const int64_t row = (int64_t)blockIdx.x * rpc + sub;
+    const bool live = row < p.N;
+    const int64_t base = live ? row * p.H : 0;
+    float v[VPT][kVec];
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int k = t + j * p.tpr;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) v[j][i] = 0.f;
+        if (live && k < p.nv) {
+            const u32x8 a = ld256_stream(p.x + base + k * kVec);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[j][2 * i] = bf16lo(a.v[i]);
+                v[j][2 * i + 1] = bf16hi(a.v[i]);
+            }
+            if (p.res) {
+                const u32x8 b = ld256_stream(p.res + base + k * kVec);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    v[j][2 * i] += bf16lo(b.v[i]);
+                    v[j][2 * i + 1] += bf16hi(b.v[i]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) ss = fmaf(v[j][i], v[j][i], ss);
+        }
+    }
+    ss = row_sum(ss, p.tpr, red);
+    const float rstd = 1.0f / sqrtf(ss * p.inv_h + p.eps);
+    if (live && t == 0 && p.rstd) p.rstd[row] = rstd;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int k = t + j * p.tpr;
+        const bool on = live && k < p.nv;  // a multiple of 8 lanes: nv is
+        u32x8 o;
+        if (on && p.h) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o.v[i] = pack_bf16x2(v[j][2 * i], v[j][2 * i + 1]);
+            st256(p.h + base + k * kVec, o);
+        }
+        float g[kVec];
+        if (on) {
+            load_gamma(p.gamma, p.gamma_fp32, k * kVec, g);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) v[j][i] = v[j][i] * rstd * g[i];
+        }
+        if (on && p.y) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o.v[i] = pack_bf16x2(v[j][2 * i], v[j][2 * i + 1]);
+            st256(p.y + base + k * kVec, o);
+        }
+        if (p.q) {
+            float amax = 1e-4f;
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) amax = fmaxf(amax, fabsf(v[j][i]));
+#pragma unroll
+            for (int off = 1; off < 8; off <<= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, off));
+            if (on) {
+                const float s = 448.0f / amax;
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    w[i] = pack_e4m3x2(v[j][4 * i] * s, v[j][4 * i + 1] * s) |
+                           pack_e4m3x2(v[j][4 * i + 2] * s, v[j][4 * i + 3] * s) << 16;
+                *reinterpret_cast<uint4*>(p.q + base + k * kVec) = make_uint4(w[0], w[1], w[2], w[3]);
+                if ((k & 7) == 0) p.q_scale[row * (p.H / 128) + k / 8] = amax / 448.0f;
+            }
+        }
+    }
+}
+
+struct NormBwdParams {
+    int64_t N;
+    int H, nv, tpr;
+    const uint16_t* h;
+    const float* rstd;
+    const void* gamma;
+    int gamma_fp32;
+    float inv_h;
+    const uint16_t* dy;
+    const uint16_t* dh;
+    uint16_t* dx;
+    float* part;  // [CTAs * rows per CTA][H]
+};
+
+// Each row slot (a CTA's rows-per-CTA of them) walks rows slot, slot + slots,
+// ... and keeps its dgamma sums in registers until the end.
+template <int VPT>
+__global__ void __launch_bounds__(1024) rmsnorm_bwd_kernel(NormBwdParams p) {
+    __shared__ float red[2][32];
+    const int rpc = blockDim.x / p.tpr;
+    const int sub = threadIdx.x / p.tpr, t = threadIdx.x - sub * p.tpr;
+    const int64_t slot = (int64_t)blockIdx.x * rpc + sub, slots = (int64_t)gridDim.x * rpc;
+    float dg[VPT][kVec];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) dg[j][i] = 0.f;
+    int flip = 0;
+    for (int64_t row0 = (int64_t)blockIdx.x * rpc; row0 < p.N; row0 += slots, flip ^= 1) {
+        const int64_t row = row0 + sub;
+        const bool live = row < p.N;
+        const int64_t base = live ? row * p.H : 0;
+        const float rstd = live ? p.rstd[row] : 0.f;
+        float n[VPT][kVec], dt[VPT][kVec];
+        float dot = 0.f;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int k = t + j * p.tpr;
+            if (live && k < p.nv) {
+                const u32x8 a = ld256_stream(p.h + base + k * kVec), b = ld256_stream(p.dy + base + k * kVec);
+                float g[kVec];
+                load_gamma(p.gamma, p.gamma_fp32, k * kVec, g);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    n[j][2 * i] = bf16lo(a.v[i]) * rstd;
+                    n[j][2 * i + 1] = bf16hi(a.v[i]) * rstd;
+                    dt[j][2 * i] = bf16lo(b.v[i]);
+                    dt[j][2 * i + 1] = bf16hi(b.v[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) {
+                    dg[j][i] = fmaf(dt[j][i], n[j][i], dg[j][i]);
+                    dt[j][i] *= g[i];
+                    dot = fmaf(dt[j][i], n[j][i], dot);
+                }
+            }
+        }
+        const float m = row_sum(dot, p.tpr, red[flip]) * p.inv_h;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int k = t + j * p.tpr;
+            if (live && k < p.nv) {
+                u32x8 c;
+                if (p.dh) c = ld256_stream(p.dh + base + k * kVec);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    float lo = rstd * (dt[j][2 * i] - n[j][2 * i] * m);
+                    float hi = rstd * (dt[j][2 * i + 1] - n[j][2 * i + 1] * m);
+                    if (p.dh) {
+                        lo += bf16lo(c.v[i]);
+                        hi += bf16hi(c.v[i]);
+                    }
+                    c.v[i] = pack_bf16x2(lo, hi);
+                }
+                st256(p.dx + base + k * kVec, c);
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int k = t + j * p.tpr;
+        if (k < p.nv) {
+            float4* o = reinterpret_cast<float4*>(p.part + slot * p.H + k * kVec);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                o[i] = make_float4(dg[j][4 * i], dg[j][4 * i + 1], dg[j][4 * i + 2], dg[j][4 * i + 3]);
+        }
+    }
+}
+
+// dgamma[c] = sum of the slots' partial rows, in slot order within each of 8
+// strides, then over the strides.
+__global__ void __launch_bounds__(256) dgamma_kernel(const float* part, int slots, int H, float* dgamma) {
+    __shared__ float s[8][33];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + lane;
+    float a = 0.f;
+    for (int i = w; i < slots; i += 8) a += part[(int64_t)i * H + c];
+    s[w][lane] = a;
+    __syncthreads();
+    if (w == 0) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) a += s[i][lane];
+        dgamma[c] = a;
+    }
+}
+
+// Threads per row (whole warps) and vectors per thread: one vector each up to
+// 512 threads, then two, then four.
+void shape_of(int H, int* nv, int* tpr, int* vpt) {
+    *nv = H / kVec;
+    *vpt = *nv <= 512 ? 1 : *nv <= 2048 ? 2 : 4;
+    *tpr = ((*nv + *vpt - 1) / *vpt + 31) / 32 * 32;
+}
+
+int rows_per_cta(int tpr) { return tpr >= 256 ? 1 : 256 / tpr; }
+
+// Partial dgamma rows of a backward call, at most.
+constexpr int64_t kMaxSlots = 1184;
+
+int64_t bwd_slots(int64_t N, int tpr) {
+    const int rpc = rows_per_cta(tpr);
+    const int64_t rows = (N + rpc - 1) / rpc * rpc;
+    const int64_t most = kMaxSlots / rpc * rpc;
+    return rows < most ? rows : most;
+}
+
+ep_status_t check_shape(int64_t N, int H, int gamma_type) {
+    if (N < 0) return fail(EP_ERR_INVALID, "N must be >= 0");
+    if (H < 128 || H % 128 != 0 || H > 65536)
+        return fail(EP_ERR_UNSUPPORTED, "H must be a multiple of 128 in [128, 65536]");
+    if (N > ((int64_t)1 << 31) - 1) return fail(EP_ERR_UNSUPPORTED, "N must be < 2^31");
+    if (gamma_type != EP_DTYPE_BF16 && gamma_type != EP_DTYPE_FP32)
+        return fail(EP_ERR_INVALID, "gamma_type must be EP_DTYPE_BF16 or EP_DTYPE_FP32");
+    return EP_OK;
+}
+
+bool misaligned(const void* p, unsigned n) { return (uintptr_t)p % n != 0; }
+
+ep_status_t launched(const char* what) {
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(EP_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
+    set_last_error("");
+    return EP_OK;
+}
+
+}  // namespace
+}  // namespace ep
+
+extern "C" {
+
+ep_status_t ep_rmsnorm(int64_t N, int H, const void* d_x, const void* d_residual, const void* d_gamma, int gamma_type,
+                       float eps, void* d_h, void* d_y, void* d_q, float* d_q_scale, float* d_rstd, void* stream) {
+    using namespace ep;
+    if (ep_status_t st = check_shape(N, H, gamma_type)) return st;
+    if (!(eps > 0.f)) return fail(EP_ERR_INVALID, "eps must be > 0");
+    if ((d_q == nullptr) != (d_q_scale == nullptr)) return fail(EP_ERR_INVALID, "d_q and d_q_scale go together");
+    if (N > 0 && !d_h && !d_y && !d_q && !d_rstd) return fail(EP_ERR_INVALID, "no output is given");
+    if (N > 0 && d_y && d_y == d_h) return fail(EP_ERR_INVALID, "d_h and d_y are the same array");
+    if (N > 0 && (!d_x || !d_gamma)) return fail(EP_ERR_INVALID, "d_x and d_gamma must be non-NULL");
+    if (misaligned(d_x, 32) || misaligned(d_residual, 32) || misaligned(d_gamma, 32) || misaligned(d_h, 32) ||
+        misaligned(d_y, 32))
+        return fail(EP_ERR_INVALID, "d_x, d_residual, d_gamma, d_h and d_y must be 32-byte aligned");
+    if (misaligned(d_q, 16)) return fail(EP_ERR_INVALID, "d_q must be 16-byte aligned");
+    if (misaligned(d_q_scale, 4) || misaligned(d_rstd, 4))
+        return fail(EP_ERR_INVALID, "d_q_scale and d_rstd must be 4-byte aligned");
+    set_last_error("");
+    if (N == 0) return EP_OK;
+    NormParams p{};
+    int vpt;
+    shape_of(H, &p.nv, &p.tpr, &vpt);
+    p.N = N;
+    p.H = H;
+    p.x = static_cast<const uint16_t*>(d_x);
+    p.res = static_cast<const uint16_t*>(d_residual);
+    p.gamma = d_gamma;
+    p.gamma_fp32 = gamma_type == EP_DTYPE_FP32;
+    p.eps = eps;
+    p.inv_h = 1.0f / (float)H;
+    p.h = static_cast<uint16_t*>(d_h);
+    p.y = static_cast<uint16_t*>(d_y);
+    p.q = static_cast<uint8_t*>(d_q);
+    p.q_scale = d_q_scale;
+    p.rstd = d_rstd;
+    const int rpc = rows_per_cta(p.tpr);
+    const unsigned grid = (unsigned)((N + rpc - 1) / rpc);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (vpt == 1) rmsnorm_kernel<1><<<grid, p.tpr * rpc, 0, s>>>(p);
+    else if (vpt == 2) rmsnorm_kernel<2><<<grid, p.tpr * rpc, 0, s>>>(p);
+    else rmsnorm_kernel<4><<<grid, p.tpr * rpc, 0, s>>>(p);
+    return launched("rmsnorm");
+}
+
+ep_status_t ep_rmsnorm_backward_workspace_bytes(int64_t N, int H, size_t* bytes) {
+    using namespace ep;
+    if (ep_status_t st = check_shape(N, H, EP_DTYPE_BF16)) return st;
+    if (!bytes) return fail(EP_ERR_INVALID, "bytes is NULL");
+    int nv, tpr, vpt;
+    shape_of(H, &nv, &tpr, &vpt);
+    *bytes = (size_t)(N > 0 ? bwd_slots(N, tpr) : 1) * H * sizeof(float);
+    set_last_error("");
+    return EP_OK;
+}
+
+ep_status_t ep_rmsnorm_backward(int64_t N, int H, const void* d_h, const float* d_rstd, const void* d_gamma,
+                                int gamma_type, const void* d_dy, const void* d_dh, void* d_dx, float* d_dgamma,
+                                void* d_workspace, size_t workspace_bytes, void* stream) {
+    using namespace ep;
+    if (ep_status_t st = check_shape(N, H, gamma_type)) return st;
+    if (!d_dgamma) return fail(EP_ERR_INVALID, "d_dgamma must be non-NULL");
+    if (N > 0 && (!d_h || !d_rstd || !d_gamma || !d_dy || !d_dx))
+        return fail(EP_ERR_INVALID, "d_h, d_rstd, d_gamma, d_dy and d_dx must be non-NULL");
+    if (misaligned(d_h, 32) || misaligned(d_gamma, 32) || misaligned(d_dy, 32) || misaligned(d_dh, 32) ||
+        misaligned(d_dx, 32))
+        return fail(EP_ERR_INVALID, "d_h, d_gamma, d_dy, d_dh and d_dx must be 32-byte aligned");
+    if (misaligned(d_rstd, 4) || misaligned(d_dgamma, 4))
+        return fail(EP_ERR_INVALID, "d_rstd and d_dgamma must be 4-byte aligned");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (N == 0) {
+        const cudaError_t e = cudaMemsetAsync(d_dgamma, 0, (size_t)H * sizeof(float), s);
+        if (e != cudaSuccess) return fail(EP_ERR_CUDA, "memset: %s", cudaGetErrorString(e));
+        set_last_error("");
+        return EP_OK;
+    }
+    size_t need = 0;
+    if (ep_status_t st = ep_rmsnorm_backward_workspace_bytes(N, H, &need)) return st;
+    if (!d_workspace || misaligned(d_workspace, 256))
+        return fail(EP_ERR_INVALID, "d_workspace must be non-NULL and 256-byte aligned");
+    if (workspace_bytes < need)
+        return fail(EP_ERR_OOM, "workspace has %zu bytes, the call needs %zu", workspace_bytes, need);
+    NormBwdParams p{};
+    int vpt;
+    shape_of(H, &p.nv, &p.tpr, &vpt);
+    p.N = N;
+    p.H = H;
+    p.h = static_cast<const uint16_t*>(d_h);
+    p.rstd = d_rstd;
+    p.gamma = d_gamma;
+    p.gamma_fp32 = gamma_type == EP_DTYPE_FP32;
+    p.inv_h = 1.0f / (float)H;
+    p.dy = static_cast<const uint16_t*>(d_dy);
+    p.dh = static_cast<const uint16_t*>(d_dh);
+    p.dx = static_cast<uint16_t*>(d_dx);
+    p.part = static_cast<float*>(d_workspace);
+    const int rpc = rows_per_cta(p.tpr);
+    const int slots = (int)bwd_slots(N, p.tpr);
+    if (vpt == 1) rmsnorm_bwd_kernel<1><<<slots / rpc, p.tpr * rpc, 0, s>>>(p);
+    else if (vpt == 2) rmsnorm_bwd_kernel<2><<<slots / rpc, p.tpr * rpc, 0, s>>>(p);
+    else rmsnorm_bwd_kernel<4><<<slots / rpc, p.tpr * rpc, 0, s>>>(p);
+    if (ep_status_t st = launched("rmsnorm backward")) return st;
+    dgamma_kernel<<<H / 32, 256, 0, s>>>(p.part, slots, H, d_dgamma);
+    return launched("dgamma");
+}
+
+}  // extern "C"

@@ -30,6 +30,9 @@ EP_FLAG_LOW_LATENCY = 0x2
 EP_FLAG_DEDUP = 0x4
 EP_FLAG_SHARD = 0x8
 EP_ROUTE_SOFTMAX, EP_ROUTE_SOFTMAX_RENORM, EP_ROUTE_GROUP_SIGMOID = 0, 1, 2
+EP_DTYPE_BF16, EP_DTYPE_FP32, EP_DTYPE_E4M3 = 0, 1, 2
+EP_SCORE_SOFTMAX, EP_SCORE_SIGMOID = 0, 1
+EP_ACT_NONE, EP_ACT_SILU, EP_ACT_GELU, EP_ACT_SWIGLU = 0, 1, 2, 3
 
 
 class EpConfig(ctypes.Structure):
@@ -43,6 +46,12 @@ class EpLayout(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "topk_idx", "topk_w", "is_token_in_rank", "num_tokens_per_rank", "cnt_src_expert",
         "num_tokens_per_expert", "expert_off", "rank_off", "src_off", "dst_row")]
+
+
+class EpLinear(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "x", "x_scale", "w", "w_scale", "bias", "residual", "out", "out_scale")] + \
+        [(n, ctypes.c_int32) for n in ("in_features", "out_features", "act", "out_type")]
 
 
 _P = ctypes.c_void_p
@@ -100,6 +109,23 @@ _lib.ep_shard_dispatch.argtypes = [_P, ctypes.c_int, ctypes.c_int, _P, _P, _P, _
 _lib.ep_shard_dispatch.restype = _st
 _lib.ep_shard_combine.argtypes = [_P, ctypes.c_int, ctypes.c_int, _P, _P, _P, _P]
 _lib.ep_shard_combine.restype = _st
+_i64, _int, _sz, _f32 = ctypes.c_int64, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
+_lib.ep_rmsnorm.argtypes = [_i64, _int, _P, _P, _P, _int, _f32, _P, _P, _P, _P, _P, _P]
+_lib.ep_rmsnorm.restype = _st
+_lib.ep_rmsnorm_backward_workspace_bytes.argtypes = [_i64, _int, ctypes.POINTER(_sz)]
+_lib.ep_rmsnorm_backward_workspace_bytes.restype = _st
+_lib.ep_rmsnorm_backward.argtypes = [_i64, _int, _P, _P, _P, _int, _P, _P, _P, _P, _P, _sz, _P]
+_lib.ep_rmsnorm_backward.restype = _st
+_lib.ep_balance_loss_workspace_bytes.argtypes = [_i64, _int, _int, ctypes.POINTER(_sz)]
+_lib.ep_balance_loss_workspace_bytes.restype = _st
+_lib.ep_balance_loss.argtypes = [_i64, _int, _int, _int, _P, _P, _int, _P, _f32, _P, _P, _P, _P, _sz, _P, _P]
+_lib.ep_balance_loss.restype = _st
+_lib.ep_balance_loss_backward.argtypes = [_i64, _int, _int, _int, _P, _int, _P, _P, _f32, _P, _int, _P, _P]
+_lib.ep_balance_loss_backward.restype = _st
+_lib.ep_linear.argtypes = [_P, _i64, ctypes.POINTER(EpLinear), _P]
+_lib.ep_linear.restype = _st
+_lib.ep_expert_linear.argtypes = [_P, _int, ctypes.POINTER(EpLinear), _P]
+_lib.ep_expert_linear.restype = _st
 
 EXPORTED = ("ep_abi_version", "ep_status_string", "ep_last_error_message", "ep_default_config",
             "ep_buffer_workspace_bytes", "ep_buffer_create", "ep_buffer_destroy", "ep_buffer_set_num_sms",
@@ -107,13 +133,17 @@ EXPORTED = ("ep_abi_version", "ep_status_string", "ep_last_error_message", "ep_d
             "ep_buffer_recv", "ep_get_layout", "ep_dispatch", "ep_combine", "ep_check_errors",
             "ep_get_layout_noalloc", "ep_selftest_wait_timeout", "ep_buffer_dedup", "ep_dispatch_dedup",
             "ep_permute", "ep_local_reduce", "ep_combine_dedup", "ep_buffer_shard", "ep_shard_layout",
-            "ep_shard_place", "ep_shard_dispatch", "ep_shard_combine")
+            "ep_shard_place", "ep_shard_dispatch", "ep_shard_combine",
+            "ep_rmsnorm", "ep_rmsnorm_backward_workspace_bytes", "ep_rmsnorm_backward",
+            "ep_balance_loss_workspace_bytes", "ep_balance_loss", "ep_balance_loss_backward",
+            "ep_linear", "ep_expert_linear")
 
 
 class EpError(RuntimeError):
-    def __init__(self, status: int, where: str):
+    def __init__(self, status: int, where: str, msg: str | None = None):
         self.status = status
-        msg = _lib.ep_last_error_message().decode()
+        if msg is None:
+            msg = _lib.ep_last_error_message().decode()
         super().__init__(f"{where}: {_lib.ep_status_string(status).decode()} ({msg})")
 
 
@@ -400,3 +430,197 @@ def ep_shard_combine(buf: EpBuffer, rank: int, T: int, peer_y, peer_y_scale, out
     ty, ts = _table(peer_y), _table(peer_y_scale)
     _check(_lib.ep_shard_combine(buf.handle, rank, T, ty, ts, _ptr(out), _stream(stream)), "ep_shard_combine")
 
+
+
+# ---- the MoE block around dispatch and combine ----------------------------------
+# These take torch tensors only, and check what a pointer cannot say: device,
+# element type, shape and contiguity.
+
+_E4M3 = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _tensor(where: str, name: str, t, dtypes, shape, device) -> None:
+    """t is None, or a contiguous tensor of one of `dtypes` on `device` whose
+    shape is `shape` (the first dimension may hold more if it is (">=", n))."""
+    if t is None:
+        return
+    dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
+    why = None
+    if not isinstance(t, torch.Tensor):
+        why = "is no tensor"
+    elif t.dtype not in dtypes:
+        why = f"has dtype {t.dtype}, not {' or '.join(str(d) for d in dtypes)}"
+    elif t.device != device or t.device.type != "cuda":
+        why = f"is on {t.device}, not on the CUDA device of the call ({device})"
+    elif not t.is_contiguous():
+        why = "is not contiguous"
+    elif shape is not None:
+        least = isinstance(shape[0], tuple)
+        want = (shape[0][1], *shape[1:]) if least else tuple(shape)
+        ok = t.dim() == len(want) and tuple(t.shape[1:]) == want[1:] and \
+            (t.shape[0] >= want[0] if least else t.shape[0] == want[0])
+        if not ok:
+            why = f"has shape {tuple(t.shape)}, not {'at least ' if least else ''}{want}"
+    if why:
+        raise EpError(EP_ERR_INVALID, where, f"{name} {why}")
+
+
+def _required(where: str, **tensors) -> None:
+    for name, t in tensors.items():
+        if not isinstance(t, torch.Tensor):
+            raise EpError(EP_ERR_INVALID, where, f"{name} is no tensor")
+
+
+def _stream_on(device, stream):
+    return torch.cuda.current_stream(device).cuda_stream if stream is None else _stream(stream)
+
+
+def ep_rmsnorm_backward_workspace_bytes(N: int, H: int) -> int:
+    n = _sz(0)
+    _check(_lib.ep_rmsnorm_backward_workspace_bytes(N, H, ctypes.byref(n)), "ep_rmsnorm_backward_workspace_bytes")
+    return n.value
+
+
+def ep_rmsnorm(x, gamma, eps: float, residual=None, h=None, y=None, q=None, q_scale=None, rstd=None,
+               stream=None) -> None:
+    """Residual addition, RMS norm and e4m3 cast of x [N, H] into whichever
+    of h, y, q + q_scale and rstd are given."""
+    w = "ep_rmsnorm"
+    _required(w, x=x, gamma=gamma)
+    _tensor(w, "x", x, torch.bfloat16, None, x.device)
+    if x.dim() != 2:
+        raise EpError(EP_ERR_INVALID, w, "x is not [N, H]")
+    N, H = x.shape
+    for name, t, dt, shape in (("gamma", gamma, (torch.bfloat16, torch.float32), (H,)),
+                               ("residual", residual, torch.bfloat16, (N, H)), ("h", h, torch.bfloat16, (N, H)),
+                               ("y", y, torch.bfloat16, (N, H)), ("q", q, _E4M3, (N, H)),
+                               ("q_scale", q_scale, torch.float32, (N, H // 128)), ("rstd", rstd, torch.float32, (N,))):
+        _tensor(w, name, t, dt, shape, x.device)
+    with torch.cuda.device(x.device):
+        _check(_lib.ep_rmsnorm(N, H, _ptr(x), _ptr(residual), _ptr(gamma), int(gamma.dtype == torch.float32), eps,
+                               _ptr(h), _ptr(y), _ptr(q), _ptr(q_scale), _ptr(rstd), _stream_on(x.device, stream)), w)
+
+
+def ep_rmsnorm_backward(h, rstd, gamma, dy, dx, dgamma, workspace, dh=None, stream=None) -> None:
+    """Gradient of ep_rmsnorm; workspace: uint8, ep_rmsnorm_backward_workspace_bytes(N, H)."""
+    w = "ep_rmsnorm_backward"
+    _required(w, h=h, rstd=rstd, gamma=gamma, dy=dy, dx=dx, dgamma=dgamma, workspace=workspace)
+    _tensor(w, "h", h, torch.bfloat16, None, h.device)
+    if h.dim() != 2:
+        raise EpError(EP_ERR_INVALID, w, "h is not [N, H]")
+    N, H = h.shape
+    for name, t, dt, shape in (("rstd", rstd, torch.float32, (N,)),
+                               ("gamma", gamma, (torch.bfloat16, torch.float32), (H,)),
+                               ("dy", dy, torch.bfloat16, (N, H)), ("dh", dh, torch.bfloat16, (N, H)),
+                               ("dx", dx, torch.bfloat16, (N, H)), ("dgamma", dgamma, torch.float32, (H,)),
+                               ("workspace", workspace, torch.uint8, None)):
+        _tensor(w, name, t, dt, shape, h.device)
+    with torch.cuda.device(h.device):
+        _check(_lib.ep_rmsnorm_backward(N, H, _ptr(h), _ptr(rstd), _ptr(gamma), int(gamma.dtype == torch.float32),
+                                        _ptr(dy), _ptr(dh), _ptr(dx), _ptr(dgamma), _ptr(workspace),
+                                        workspace.numel(), _stream_on(h.device, stream)), w)
+
+
+def ep_balance_loss_workspace_bytes(N: int, E: int, S: int = 1) -> int:
+    n = _sz(0)
+    _check(_lib.ep_balance_loss_workspace_bytes(N, E, S, ctypes.byref(n)), "ep_balance_loss_workspace_bytes")
+    return n.value
+
+
+def _sequences(where, seq_off, device) -> int:
+    if seq_off is None:
+        return 1
+    _tensor(where, "seq_off", seq_off, torch.int32, None, device)
+    if seq_off.dim() != 1 or seq_off.numel() < 2:
+        raise EpError(EP_ERR_INVALID, where, "seq_off is not [S + 1] with S >= 1")
+    return seq_off.numel() - 1
+
+
+def ep_balance_loss(logits, topk_idx, score: int, coef: float, loss, counts, workspace, error_word, seq_off=None,
+                    prob=None, stream=None) -> None:
+    """Balance loss of logits [N, E] and topk_idx [N, K] over the sequences of
+    seq_off [S + 1] (None: one); fills loss [1], counts [S, E], prob [S, E]."""
+    w = "ep_balance_loss"
+    _required(w, logits=logits, topk_idx=topk_idx, loss=loss, counts=counts, workspace=workspace,
+              error_word=error_word)
+    if logits.dim() != 2 or topk_idx.dim() != 2:
+        raise EpError(EP_ERR_INVALID, w, "logits is not [N, E], or topk_idx not [N, K]")
+    dev = logits.device
+    (N, E), K, S = logits.shape, topk_idx.shape[1], _sequences(w, seq_off, dev)
+    for name, t, dt, shape in (("logits", logits, torch.float32, (N, E)), ("topk_idx", topk_idx, torch.int32, (N, K)),
+                               ("loss", loss, torch.float32, (1,)), ("counts", counts, torch.int32, (S, E)),
+                               ("prob", prob, torch.float32, (S, E)), ("workspace", workspace, torch.uint8, None),
+                               ("error_word", error_word, (torch.int32, torch.uint32), (1,))):
+        _tensor(w, name, t, dt, shape, dev)
+    with torch.cuda.device(dev):
+        _check(_lib.ep_balance_loss(N, E, K, score, _ptr(logits), _ptr(topk_idx), S, _ptr(seq_off), coef, _ptr(loss),
+                                    _ptr(counts), _ptr(prob), _ptr(workspace), workspace.numel(), _ptr(error_word),
+                                    _stream_on(dev, stream)), w)
+
+
+def ep_balance_loss_backward(logits, counts, topk: int, score: int, coef: float, dlogits, seq_off=None,
+                             grad_loss=None, accumulate: bool = False, stream=None) -> None:
+    """Gradient of ep_balance_loss for the logits, into (or added to) dlogits."""
+    w = "ep_balance_loss_backward"
+    _required(w, logits=logits, counts=counts, dlogits=dlogits)
+    if logits.dim() != 2:
+        raise EpError(EP_ERR_INVALID, w, "logits is not [N, E]")
+    dev = logits.device
+    (N, E), S = logits.shape, _sequences(w, seq_off, dev)
+    for name, t, dt, shape in (("logits", logits, torch.float32, (N, E)), ("counts", counts, torch.int32, (S, E)),
+                               ("dlogits", dlogits, torch.float32, (N, E)),
+                               ("grad_loss", grad_loss, torch.float32, (1,))):
+        _tensor(w, name, t, dt, shape, dev)
+    with torch.cuda.device(dev):
+        _check(_lib.ep_balance_loss_backward(N, E, topk, score, _ptr(logits), S, _ptr(seq_off), _ptr(counts), coef,
+                                             _ptr(grad_loss), 1 if accumulate else 0, _ptr(dlogits),
+                                             _stream_on(dev, stream)), w)
+
+
+def _linear_args(where, buf, groups, rows, x, w, out, x_scale, w_scale, bias, residual, act, out_scale):
+    """Checks the tensors of a linear layer on `rows` rows (at least) and
+    returns the C struct."""
+    _required(where, x=x, w=w, out=out)
+    dev = buf.workspace.device
+    if x.dim() != 2 or w.dim() != 3 or out.dim() != 2:
+        raise EpError(EP_ERR_INVALID, where, "x, w, out are not [rows, in], [G, wide, in], [rows, out]")
+    cin, cout = x.shape[1], out.shape[1]
+    parts = 2 if act == EP_ACT_SWIGLU else 1
+    if (x_scale is None) != (w_scale is None):
+        raise EpError(EP_ERR_INVALID, where, "x_scale and w_scale go together")
+    kind = torch.bfloat16 if x_scale is None else _E4M3
+    outs = {torch.bfloat16: EP_DTYPE_BF16, torch.float32: EP_DTYPE_FP32}
+    n = (">=", rows)
+    for name, t, dt, shape in (("x", x, kind, (n, cin)), ("w", w, kind, (groups, parts * cout, cin)),
+                               ("x_scale", x_scale, torch.float32, (n, cin // 128)),
+                               ("w_scale", w_scale, torch.float32, (groups, parts * -(-cout // 128), cin // 128)),
+                               ("bias", bias, torch.float32, (groups, parts * cout)),
+                               ("residual", residual, torch.bfloat16, (n, cout)),
+                               ("out", out, (torch.bfloat16, torch.float32, *_E4M3), (n, cout)),
+                               ("out_scale", out_scale, torch.float32, (n, cout // 128))):
+        _tensor(where, name, t, dt, shape, dev)
+    return EpLinear(x=_ptr(x), x_scale=_ptr(x_scale), w=_ptr(w), w_scale=_ptr(w_scale), bias=_ptr(bias),
+                    residual=_ptr(residual), out=_ptr(out), out_scale=_ptr(out_scale), in_features=cin,
+                    out_features=cout, act=act, out_type=outs.get(out.dtype, EP_DTYPE_E4M3))
+
+
+def ep_linear(buf: EpBuffer, x, w, out, x_scale=None, w_scale=None, bias=None, residual=None,
+              act: int = EP_ACT_NONE, out_scale=None, stream=None) -> None:
+    """out = act(x w[0]^T + bias) + residual on x [rows, in]; w [1, wide, in]."""
+    rows = x.shape[0] if isinstance(x, torch.Tensor) and x.dim() == 2 else 0
+    a = _linear_args("ep_linear", buf, 1, rows, x, w, out, x_scale, w_scale, bias, residual, act, out_scale)
+    _check(_lib.ep_linear(buf.handle, rows, ctypes.byref(a), _stream_on(buf.workspace.device, stream)), "ep_linear")
+
+
+def ep_expert_linear(buf: EpBuffer, T: int, x, w, out, x_scale=None, w_scale=None, bias=None, residual=None,
+                     act: int = EP_ACT_NONE, out_scale=None, stream=None) -> None:
+    """The experts' layer on the receive rows of the last layout: x [rows, in],
+    w [experts, wide, in] (a shard's own experts with EP_FLAG_SHARD)."""
+    c = buf.cfg
+    ll = bool(c.flags & EP_FLAG_LOW_LATENCY)
+    rows = c.num_experts * c.num_ranks * c.max_tokens_per_rank if ll else c.num_ranks * T * c.topk
+    groups = c.num_experts // c.num_ranks if buf.shard else c.num_experts
+    a = _linear_args("ep_expert_linear", buf, groups, rows, x, w, out, x_scale, w_scale, bias, residual, act,
+                     out_scale)
+    _check(_lib.ep_expert_linear(buf.handle, T, ctypes.byref(a), _stream_on(buf.workspace.device, stream)),
+           "ep_expert_linear")

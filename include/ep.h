@@ -378,6 +378,180 @@ ep_status_t ep_shard_dispatch(ep_buffer_t *buf, int rank, int T, const void *d_x
 ep_status_t ep_shard_combine(ep_buffer_t *buf, int rank, int T, const void *const *peer_y,
                              const float *const *peer_y_scale, void *d_out, void *stream);
 
+/* ---- the MoE block around dispatch and combine ------------------------------
+ * The steps a block runs beside routing, dispatch and combine: the norm in
+ * front of the router, the linear layers (router projection, shared expert,
+ * the routed experts on the receive rows) and the router's balance loss.
+ * Every call below is stream-ordered and captures into a CUDA graph. Calls
+ * without a buffer run on the current device, which `stream` must belong to.
+ * No call keeps state between calls: two calls may overlap on the GPU if they
+ * share no output and no workspace. Outputs may not overlap inputs or each
+ * other unless a call says so. A call on zero rows launches nothing, and
+ * writes nothing unless it says so. */
+
+/* Element types of the calls below. */
+typedef enum {
+    EP_DTYPE_BF16 = 0,
+    EP_DTYPE_FP32 = 1,
+    EP_DTYPE_E4M3 = 2 /* e4m3 values with fp32 scales beside them */
+} ep_dtype_t;
+
+/* Residual addition, RMS norm, e4m3 cast, on N rows of H channels:
+ *   v = x + residual  (residual NULL: v = x)
+ *   rstd = 1 / sqrt(mean(v^2) + eps)
+ *   n = v * rstd * gamma
+ *   h = bf16_rne(v); y = bf16_rne(n)
+ *   q, q_scale = the cast of ep_dispatch of n (from fp32, not from y), one
+ *                scale per 128 channels
+ * Sums and v are fp32; nothing is rounded before an output is.
+ *  - d_x, d_residual: bf16 [N, H]; d_gamma: [H], bf16 or fp32 (gamma_type);
+ *  - d_h, d_y: bf16 [N, H]; d_q: e4m3 [N, H] with d_q_scale fp32 [N, H/128];
+ *    d_rstd: fp32 [N]. Each is optional (NULL), q and q_scale go together, and
+ *    at least one output is given.
+ * d_h may be d_x or d_residual itself (in place), and so may d_y where d_h is
+ * not that same array. H: a multiple of 128, at most 65536. eps > 0. x,
+ * residual, h, y and gamma are 32-byte aligned, q 16-byte.
+ * Errors: EP_ERR_INVALID, EP_ERR_UNSUPPORTED (H). */
+ep_status_t ep_rmsnorm(int64_t N, int H, const void *d_x, const void *d_residual, const void *d_gamma,
+                       int gamma_type, float eps, void *d_h, void *d_y, void *d_q, float *d_q_scale,
+                       float *d_rstd, void *stream);
+
+/* Bytes of the workspace that ep_rmsnorm_backward takes for N rows of H. */
+ep_status_t ep_rmsnorm_backward_workspace_bytes(int64_t N, int H, size_t *bytes);
+
+/* Gradient of ep_rmsnorm. h is its normalised input (d_h, or d_x where it had
+ * no residual) and rstd its d_rstd. With n = h * rstd and t = dy * gamma:
+ *   dx = bf16_rne(rstd * (t - n * mean(t * n)) + dh)
+ *   dgamma = sum over rows of dy * n  (fp32, in an order that N, H and the
+ *            GPU fix: the same call gives the same bits)
+ * (n differs from the forward's by h's rounding alone.)
+ * dx is the gradient of x and of the residual alike. dh is the gradient that
+ * reaches h from later layers (NULL: none). The e4m3 cast passes gradients
+ * straight through, so dy is the gradient of y, or of q's values.
+ *  - d_h, d_dy, d_dh, d_dx: bf16 [N, H]; d_rstd: fp32 [N]; d_gamma: [H] of
+ *    gamma_type; d_dgamma: fp32 [H], overwritten; zeros if N is 0.
+ *  - d_workspace: 256-byte aligned, at least the bytes named above. Calls that
+ *    may overlap need one each.
+ * d_dx may be d_dy or d_dh itself. Alignment as for ep_rmsnorm.
+ * Errors: EP_ERR_INVALID, EP_ERR_UNSUPPORTED (H), EP_ERR_OOM (workspace). */
+ep_status_t ep_rmsnorm_backward(int64_t N, int H, const void *d_h, const float *d_rstd, const void *d_gamma,
+                                int gamma_type, const void *d_dy, const void *d_dh, void *d_dx, float *d_dgamma,
+                                void *d_workspace, size_t workspace_bytes, void *stream);
+
+/* Scores of the balance loss. z: a token's E router logits. */
+typedef enum {
+    EP_SCORE_SOFTMAX = 0, /* p = softmax(z) */
+    EP_SCORE_SIGMOID = 1  /* p_e = sigmoid(z_e) / sum_j sigmoid(z_j) */
+} ep_score_t;
+
+/* Bytes of the workspace that ep_balance_loss takes. */
+ep_status_t ep_balance_loss_workspace_bytes(int64_t N, int E, int S, size_t *bytes);
+
+/* Balance loss of the router over S sequences, with the per-expert counts.
+ * Sequence s holds the tokens [seq_off[s], seq_off[s+1]), T_s of them:
+ *   counts[s][e] = slots of its tokens with topk_idx = e (masked slots, -1, count nowhere)
+ *   f_se = counts[s][e] * E / (K * T_s)
+ *   prob[s][e] = mean over its tokens of p_te
+ *   loss = coef / S * sum over s, e of f_se * prob[s][e]
+ * An empty sequence adds 0 and gets zero counts and prob. A token counts
+ * towards T_s and prob even if all its slots are masked.
+ *  - d_logits: fp32 [N, E]; d_topk_idx: int32 [N, K] (as ep_get_layout leaves
+ *    them in ep_layout_t). Logits are finite; E up to 1024, K up to 32.
+ *  - d_seq_off: int32 [S+1], non-decreasing, within [0, N]; tokens outside
+ *    [seq_off[0], seq_off[S]) are read by nothing. NULL with S = 1: one
+ *    sequence of all N tokens.
+ *  - d_loss: fp32 [1]; d_counts: int32 [S, E]; d_prob: fp32 [S, E] or NULL.
+ *    They are written for N = 0 too. The same call gives the same bits.
+ *  - d_workspace: 256-byte aligned, as ep_balance_loss_workspace_bytes says.
+ *    Calls that may overlap need one each.
+ *  - d_error_word: a device uint32, atomicOr of EP_DEVERR_EXPERT_ID (an id
+ *    outside [-1, E), counted nowhere) and EP_DEVERR_ROW_BOUNDS (seq_off out
+ *    of order or range; it is clamped into range, and the results of that
+ *    call are not defined). The caller zeroes and reads it.
+ * Errors: EP_ERR_INVALID, EP_ERR_UNSUPPORTED (E, N, S), EP_ERR_OOM (workspace). */
+ep_status_t ep_balance_loss(int64_t N, int E, int K, int score, const float *d_logits, const int32_t *d_topk_idx,
+                            int S, const int32_t *d_seq_off, float coef, float *d_loss, int32_t *d_counts,
+                            float *d_prob, void *d_workspace, size_t workspace_bytes, uint32_t *d_error_word,
+                            void *stream);
+
+/* Gradient of ep_balance_loss for the logits (the counts have none):
+ *   g = grad_loss * coef / (S * T_s)
+ *   dlogits[t][e] = g * p_te * m_te * (f_se - sum over j of f_sj * p_tj)
+ * with m = 1 (softmax) or 1 - sigmoid(z_te) (sigmoid).
+ *  - d_counts: int32 [S, E] of the forward call (or summed over ranks, with
+ *    T_s-scaled coef to match); d_grad_loss: fp32 [1] on the device, NULL = 1;
+ *  - accumulate != 0 adds to d_dlogits (fp32 [N, E]), 0 overwrites. Rows
+ *    outside every sequence are left as they were.
+ *  - d_seq_off out of order or range is clamped into range.
+ * Errors: EP_ERR_INVALID, EP_ERR_UNSUPPORTED. */
+ep_status_t ep_balance_loss_backward(int64_t N, int E, int K, int score, const float *d_logits, int S,
+                                     const int32_t *d_seq_off, const int32_t *d_counts, float coef,
+                                     const float *d_grad_loss, int accumulate, float *d_dlogits, void *stream);
+
+/* Activation in a linear layer's epilogue. */
+typedef enum {
+    EP_ACT_NONE = 0,
+    EP_ACT_SILU = 1,  /* z * sigmoid(z) */
+    EP_ACT_GELU = 2,  /* z * Phi(z), the exact (erf) form */
+    EP_ACT_SWIGLU = 3 /* silu(gate) * up: the weight holds out_features gate rows, then as many up rows */
+} ep_act_t;
+
+/* One linear layer: out = act(x W^T + bias) + residual.
+ * `wide` is out_features, or 2*out_features for EP_ACT_SWIGLU. G is the
+ * number of weight matrices: 1 for ep_linear, the experts for ep_expert_linear.
+ *  - bf16: x [rows, in_features] and w [G, wide, in_features] are bf16, with
+ *    x_scale and w_scale NULL. in_features is a multiple of 8.
+ *  - e4m3: x is e4m3 with x_scale fp32 [rows, in_features/128] (as dispatch
+ *    leaves receive rows) and w is e4m3 with w_scale fp32
+ *    [G, parts, ceil(out_features/128), in_features/128], one scale per 128 x
+ *    128 block (parts = wide/out_features: each half has its own blocks).
+ *    in_features is a multiple of 128.
+ *  - bias: fp32 [G, wide] or NULL; residual: bf16 [rows, out_features] or NULL.
+ *  - out: [rows, out_features] of out_type. EP_DTYPE_E4M3 needs out_features a
+ *    multiple of 128 and out_scale fp32 [rows, out_features/128]: the cast of
+ *    ep_dispatch, from fp32. Otherwise out_scale is NULL.
+ * Products of bf16 or e4m3 values are exact and summed in fp32 (e4m3: per 128
+ * channels, then scaled and summed); the epilogue is fp32 with one rounding at
+ * the end. Rows are contiguous. x and w are 16-byte aligned, out and residual
+ * 16-byte, scales and bias 4-byte. out may be residual itself where out_type
+ * is EP_DTYPE_BF16. */
+typedef struct {
+    const void *x;
+    const float *x_scale;
+    const void *w;
+    const float *w_scale;
+    const float *bias;
+    const void *residual;
+    void *out;
+    float *out_scale;
+    int32_t in_features;
+    int32_t out_features;
+    int32_t act;      /* ep_act_t */
+    int32_t out_type; /* ep_dtype_t */
+} ep_linear_t;
+
+/* Dense layer on `rows` rows: the router projection (fp32 out, which
+ * ep_get_layout takes as logits), a shared expert. buf gives the device and
+ * the error word; its layout is not used.
+ * Errors: EP_ERR_INVALID, EP_ERR_UNSUPPORTED. */
+ep_status_t ep_linear(ep_buffer_t *buf, int64_t rows, const ep_linear_t *p, void *stream);
+
+/* The experts' layer on receive rows: each row goes through its expert's
+ * weights. x, residual and out have the rows of ep_buffer_recv, in the order
+ * of the last layout (the row counts are read on the device):
+ *  - a standard or dedup buffer: w holds all E experts, rows expert_off;
+ *  - EP_FLAG_LOW_LATENCY: w holds all E experts, rows in the fixed (expert,
+ *    source rank) regions, each filled as cnt_src_expert says;
+ *  - EP_FLAG_SHARD (after ep_shard_place): w holds this rank's E/R experts,
+ *    rows recv_off.
+ * x, x_scale and residual hold at least R*T*K rows (low latency: M_max), even
+ * where masked slots leave the last of them unused: unused rows may be read,
+ * but reach no output. Rows that hold no slot are left as they were in out and
+ * out_scale. T is that of the last ep_get_layout or ep_shard_layout.
+ * Errors: EP_ERR_INVALID, EP_ERR_UNSUPPORTED. A wait inside the kernel that
+ * gave up sets EP_DEVERR_TIMEOUT. */
+ep_status_t ep_expert_linear(ep_buffer_t *buf, int T, const ep_linear_t *p, void *stream);
+
 /* Diagnostic: proves that the library's bounded waits end. Runs, each with a
  * limit of limit_ns (1 us .. 2 s):
  *  - the layout's grid barrier on 2 CTAs with a target that can never be
