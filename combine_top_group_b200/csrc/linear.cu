@@ -1,11 +1,26 @@
 // ep_linear and ep_expert_linear: out = act(x W^T + bias) + residual on dense
 // rows or on the experts' receive rows, bf16 or e4m3 with scales.
+//
+// The product is taken as W x^T: output channels are the 128 lanes of a
+// tensor-memory tile, rows of x its columns. Experts get any number of rows,
+// and the column count of a tcgen05 product can be any multiple of 16, so a
+// ragged last tile costs only its own columns, and a decode batch of a few
+// rows per expert wastes no lanes. Rows of W are never ragged across experts.
+//
+// One persistent CTA per SM: a warp loads tiles with TMA into a ring of shared
+// memory stages, a warp issues the products, eight warps read finished
+// accumulators out of tensor memory, where a second set fills meanwhile.
+//  - bf16: the whole sum over in_features stays in tensor memory.
+//  - e4m3: each block of 128 channels is summed on its own in tensor memory
+//    and leaves it times its scales (row scale x weight block scale, fp32)
+//    into fp32 registers, since the scales differ from block to block.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include "common.cuh"
 #include "ep.h"
 #include "internal.h"
+#include "tcgen05.cuh"
 
 namespace ep {
 namespace {
@@ -30,6 +45,15 @@ struct LinearParams {
     int64_t rows;          // dense: the one group's rows
     int64_t row_limit;     // rows the arrays hold
     uint32_t* err;
+    // shape of the launch
+    int bn;        // rows of x per tile: 32, 64 or 128
+    int na;        // 128-channel weight tiles per CTA tile: gate and up, or neighbours
+    int nt;        // channel tiles: out_features over 128 (swiglu) or 128 * na
+    int stages;    // of the shared-memory ring
+    int kblocks;   // 128-byte blocks of in_features
+    int splits;    // CTAs of a cluster that share a tile's in_features
+    uint32_t cols; // tensor-memory columns
+    int vec;       // rows of out and residual allow 4-channel accesses
 };
 
 // Rows [start, start + count) of group g, kept inside [0, row_limit).
@@ -53,105 +77,468 @@ __device__ __forceinline__ float activate(int act, float z) {
     return z;
 }
 
-__device__ __forceinline__ float e4m3_value(uint8_t b) { return unpack_e4m3x2(b).x; }
 
-constexpr int kTile = 64;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (kEpiWarps + 3);  // + loads, products, e4m3 scales
+constexpr int kSub = 128 * 128;                 // bytes of a 128-channel weight tile of one stage
+constexpr int kMaxStages = 10;
+constexpr int kMaxBn = 128;
+// Shared memory: ring | staging (unsplit) | barriers and scales.
+constexpr int kStaging = 32 * 256 * 4;
+constexpr int kScales = 2 * 2 * kMaxBn * 4;
+constexpr int kControl = 256 + kScales;
+constexpr int kSmemMax = 227 * 1024;
 
-// 64 rows x 128 out channels of one group per CTA, fp32 on the CUDA cores.
-// blockIdx = (out-channel tile, row tile of the group, group); a CTA walks
-// the group's row tiles with the stride of the grid.
-__global__ void __launch_bounds__(256) linear_kernel(LinearParams p) {
-    __shared__ float xs[16][kTile + 1];
-    __shared__ float wsm[2][16][128 + 1];
-    __shared__ float red[kTile][4];
-    int64_t start;
-    int count;
-    group_rows(p, blockIdx.z, start, count);
-    const int g = blockIdx.z / p.R;
-    const int n0 = blockIdx.x * 128;
-    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;  // 4 channels tx + 32 j, 8 rows ty + 8 i
-    const bool f8 = p.x_scale != nullptr;
-    const int kb = p.K / 128, nb = (p.N + 127) / 128;
-    for (int r0 = blockIdx.y * kTile; r0 < count; r0 += gridDim.y * kTile) {
-        float acc[2][8][4] = {};
-        for (int k0 = 0; k0 < p.K; k0 += 16) {
-            __syncthreads();
-            for (int i = threadIdx.x; i < kTile * 16; i += 256) {
-                const int r = i / 16, k = i % 16;
-                float v = 0.f;
-                if (r0 + r < count && k0 + k < p.K) {
-                    const int64_t at = (start + r0 + r) * p.K + k0 + k;
-                    v = f8 ? e4m3_value(static_cast<const uint8_t*>(p.x)[at]) *
-                                 p.x_scale[(start + r0 + r) * kb + (k0 + k) / 128]
-                           : __uint_as_float((uint32_t) static_cast<const uint16_t*>(p.x)[at] << 16);
-                }
-                xs[k][r] = v;
-            }
-            for (int h = 0; h < p.parts; ++h)
-                for (int i = threadIdx.x; i < 128 * 16; i += 256) {
-                    const int n = i / 16, k = i % 16;
-                    float v = 0.f;
-                    if (n0 + n < p.N && k0 + k < p.K) {
-                        const int64_t at = ((int64_t)g * p.wide + (int64_t)h * p.N + n0 + n) * p.K + k0 + k;
-                        v = f8 ? e4m3_value(static_cast<const uint8_t*>(p.w)[at]) *
-                                     p.w_scale[((int64_t)(g * p.parts + h) * nb + blockIdx.x) * kb + (k0 + k) / 128]
-                               : __uint_as_float((uint32_t) static_cast<const uint16_t*>(p.w)[at] << 16);
-                    }
-                    wsm[h][k][n] = v;
-                }
-            __syncthreads();
-            for (int k = 0; k < 16; ++k)
-                for (int h = 0; h < 2; ++h) {
-                    if (h >= p.parts) break;
+__host__ __device__ constexpr int stage_bytes(int na, int bn) { return na * kSub + bn * 128; }
+
+// Walks the tiles of all groups in order: a group's channel tiles, and within
+// one the row tiles, so that CTAs running together share weights through L2.
+// One warp holds 32 groups at a time.
+struct Cursor {
+    int g0 = -32;
+    int base = 0, total = 0;  // tiles before the window, and in it
+    int incl = 0, mine = 0;   // of the lane's group: tiles up to and with it, its own
+    int64_t start = 0;
+    int count = 0;
+};
+struct Tile {
+    int group, n;          // group, channel tile
+    int64_t row;           // first row of x
+    int rows;              // valid rows, at most bn
+};
+
+__device__ __forceinline__ bool find_tile(const LinearParams& p, Cursor& c, int id, Tile& t) {
+    const int lane = threadIdx.x & 31;
+    while (id >= c.base + c.total) {
+        c.base += c.total;
+        c.g0 += 32;
+        if (c.g0 >= p.G) return false;
+        c.start = 0;
+        c.count = 0;
+        if (c.g0 + lane < p.G) group_rows(p, c.g0 + lane, c.start, c.count);
+        c.mine = (c.count + p.bn - 1) / p.bn * p.nt;
+        c.incl = c.mine;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            acc[h][i][j] = fmaf(xs[k][ty + 8 * i], wsm[h][k][tx + 32 * j], acc[h][i][j]);
-                }
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(FULL, c.incl, o);
+            if (lane >= o) c.incl += v;
         }
+        c.total = __shfl_sync(FULL, c.incl, 31);
+    }
+    const int in_window = id - c.base;
+    const int src = __ffs(__ballot_sync(FULL, in_window < c.incl)) - 1;
+    const int at = in_window - (__shfl_sync(FULL, c.incl, src) - __shfl_sync(FULL, c.mine, src));
+    const int count = __shfl_sync(FULL, c.count, src);
+    const int64_t start = __shfl_sync(FULL, c.start, src);
+    const int tt = (count + p.bn - 1) / p.bn;
+    t.group = c.g0 + src;
+    t.n = at / tt;
+    const int r = (at - t.n * tt) * p.bn;
+    t.row = start + r;
+    t.rows = min(p.bn, count - r);
+    return true;
+}
+
+// Weight tiles of a CTA tile that hold channels.
+__device__ __forceinline__ int subs_of(const LinearParams& p, const Tile& t) {
+    if (p.parts == 2) return 2;
+    return p.na == 2 && (t.n * 2 + 1) * 128 < p.N ? 2 : 1;
+}
+// First channel of sub-tile `sub` within its half.
+__device__ __forceinline__ int channel_of(const LinearParams& p, const Tile& t, int sub) {
+    return p.parts == 2 ? t.n * 128 : (t.n * p.na + sub) * 128;
+}
+
+struct Bias {
+    float v[2][4];
+};
+__device__ __forceinline__ void load_bias(const LinearParams& p, const Tile& t, int subs, Bias& b) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = ty + 8 * i;
-            const int64_t row = start + r0 + r;
-            const bool live = r0 + r < count;
-            float v[4], amax = 1e-4f;
+    for (int s = 0; s < 2; ++s)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int n = n0 + tx + 32 * j;
-                v[j] = 0.f;
-                if (!live || n >= p.N) continue;
-                float z = acc[0][i][j];
-                if (p.bias) z += p.bias[(int64_t)g * p.wide + n];
-                if (p.act == EP_ACT_SWIGLU) {
-                    float u = acc[1][i][j];
-                    if (p.bias) u += p.bias[(int64_t)g * p.wide + p.N + n];
-                    v[j] = activate(EP_ACT_SILU, z) * u;
-                } else {
-                    v[j] = activate(p.act, z);
+        for (int i = 0; i < 4; ++i) {
+            b.v[s][i] = 0.f;
+            const int n = channel_of(p, t, s) + lane * 4 + i;
+            if (p.bias && s < subs && n < p.N)
+                b.v[s][i] = p.bias[(int64_t)(t.group / p.R) * p.wide + (p.parts == 2 ? s * p.N : 0) + n];
+        }
+}
+
+// One row of 128 channels, 4 to a lane: activation, residual, rounding, store.
+__device__ __forceinline__ void emit(const LinearParams& p, int64_t row, int n, float (&z)[4], const float (&u)[4]) {
+    const int lane = threadIdx.x & 31;
+    n += lane * 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        z[i] = p.act == EP_ACT_SWIGLU ? activate(EP_ACT_SILU, z[i]) * u[i] : activate(p.act, z[i]);
+    const int64_t at = row * p.N + n;
+    if (p.vec) {
+        if (p.res && n < p.N) {
+            const uint2 r = *reinterpret_cast<const uint2*>(p.res + at);
+            z[0] += bf16lo(r.x);
+            z[1] += bf16hi(r.x);
+            z[2] += bf16lo(r.y);
+            z[3] += bf16hi(r.y);
+        }
+        if (p.out_type == EP_DTYPE_E4M3) {  // out_features is a multiple of 128: every lane holds channels
+            float amax = fmaxf(fmaxf(fabsf(z[0]), fabsf(z[1])), fmaxf(fabsf(z[2]), fabsf(z[3])));
+            amax = fmaxf(amax, 1e-4f);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, o));
+            const float s = 448.0f / amax;
+            *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + at) =
+                pack_e4m3x2(z[0] * s, z[1] * s) | pack_e4m3x2(z[2] * s, z[3] * s) << 16;
+            if (lane == 0) p.out_scale[row * (p.N / 128) + n / 128] = amax / 448.0f;
+        } else if (n < p.N) {
+            if (p.out_type == EP_DTYPE_FP32)
+                *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(z[0], z[1], z[2], z[3]);
+            else
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
+                    make_uint2(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]));
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (n + i >= p.N) continue;
+        if (p.res) z[i] += __uint_as_float((uint32_t)p.res[at + i] << 16);
+        if (p.out_type == EP_DTYPE_FP32) static_cast<float*>(p.out)[at + i] = z[i];
+        else static_cast<uint16_t*>(p.out)[at + i] = (uint16_t)(pack_bf16x2(z[i], 0.f) & 0xffff);
+    }
+}
+
+// A staged row: gate and up 128 channels each, or two neighbouring tiles.
+template <typename Load>
+__device__ __forceinline__ void emit_row(const LinearParams& p, const Tile& t, int subs, const Bias& b, int64_t row,
+                                         Load load) {
+    float z[2][4];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const float4 v = s < subs ? load(s) : make_float4(0.f, 0.f, 0.f, 0.f);
+        z[s][0] = v.x + b.v[s][0];
+        z[s][1] = v.y + b.v[s][1];
+        z[s][2] = v.z + b.v[s][2];
+        z[s][3] = v.w + b.v[s][3];
+    }
+    emit(p, row, channel_of(p, t, 0), z[0], z[1]);
+    if (p.parts == 1 && subs == 2) emit(p, row, channel_of(p, t, 1), z[1], z[0]);
+}
+
+// Barrier of the epilogue warps; the _and form tells whether all of them are ok.
+__device__ __forceinline__ bool epi_sync_and(bool ok) {
+    uint32_t r;
+    asm volatile(
+        "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.cta.red.and.pred q, 1, %2, p; selp.u32 %0, 1, 0, q; }"
+        : "=r"(r)
+        : "r"((uint32_t)ok), "n"(kEpiWarps * 32)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory"); }
+
+template <bool F8, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, LinearParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    const int sb = stage_bytes(p.na, p.bn);
+    // swizzled tiles start on 1024 bytes (the same offset in every CTA of a cluster)
+    const uint32_t ring = (tc::smem_u32(smem_raw) + 1023) & ~1023u;
+    uint8_t* smem = smem_raw + (ring - tc::smem_u32(smem_raw));
+    uint8_t* after = smem + (size_t)p.stages * sb;
+    float* staging = reinterpret_cast<float*>(SPLIT ? smem : after);
+    uint8_t* control = after + (SPLIT ? 0 : kStaging);
+    float* scales = reinterpret_cast<float*>(control + 256);  // [2][2][kMaxBn]
+    volatile uint32_t* stop = reinterpret_cast<uint32_t*>(control + 244);
+    const uint32_t bars = tc::smem_u32(control);
+    auto full = [&](int s) { return bars + 8 * s; };
+    auto empty = [&](int s) { return bars + 8 * (kMaxStages + s); };
+    auto acc_full = [&](int s) { return bars + 8 * (2 * kMaxStages + s); };
+    auto acc_empty = [&](int s) { return bars + 8 * (2 * kMaxStages + 2 + s); };
+    auto scale_full = [&](int s) { return bars + 8 * (2 * kMaxStages + 4 + s); };
+    const uint32_t drained = bars + 8 * (2 * kMaxStages + 6);
+    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(control + 240);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            tc::bar_init(full(s), 1);
+            tc::bar_init(empty(s), 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            tc::bar_init(acc_full(s), 1);
+            tc::bar_init(acc_empty(s), kEpiWarps);
+            tc::bar_init(scale_full(s), 32);
+        }
+        tc::bar_init(drained, 1);
+        *stop = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kEpiWarps + 1) tc::tmem_alloc(tc::smem_u32(tmem_at), p.cols);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = *tmem_at;
+
+    const int rank = SPLIT ? (int)tc::cluster_rank() : 0;
+    const int first = SPLIT ? blockIdx.x / p.splits : blockIdx.x;
+    // a split launch has a cluster for each tile there can be
+    const int step = SPLIT ? 1 << 30 : gridDim.x;
+    const int k_lo = SPLIT ? (int)((int64_t)p.kblocks * rank / p.splits) : 0;
+    const int k_hi = SPLIT ? (int)((int64_t)p.kblocks * (rank + 1) / p.splits) : p.kblocks;
+    constexpr int kElems = F8 ? 128 : 64;  // in_features of a block
+    Cursor cur;
+    Tile t;
+
+    if (warp == kEpiWarps) {  // loads
+        int i = 0;
+        bool ok = true;
+        for (int id = first; ok && find_tile(p, cur, id, t); id += step) {
+            const int subs = subs_of(p, t);
+            const uint32_t bytes = subs * kSub + p.bn * 128;
+            if (lane == 0) {
+                for (int k = k_lo; k < k_hi; ++k, ++i) {
+                    const int s = i % p.stages;
+                    if (i >= p.stages && !tc::bar_wait(empty(s), (i / p.stages - 1) & 1, stop)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t at = ring + s * sb;
+                    tc::bar_expect(full(s), bytes);
+                    for (int a = 0; a < subs; ++a)
+                        tc::tma_4d(at + a * kSub, &map_w, full(s), k * kElems, channel_of(p, t, a), p.parts == 2 ? a : 0,
+                                   t.group / p.R);
+                    tc::tma_2d(at + p.na * kSub, &map_x, full(s), k * kElems, (int)t.row);
                 }
-                if (p.res) v[j] += __uint_as_float((uint32_t)p.res[row * p.N + n] << 16);
-                amax = fmaxf(amax, fabsf(v[j]));
+                if (!ok)  // copies in flight land before the CTA leaves
+                    for (int j = i > p.stages ? i - p.stages : 0; j < i; ++j)
+                        tc::bar_drain(full(j % p.stages), (j / p.stages) & 1);
             }
-            if (p.out_type == EP_DTYPE_E4M3) {
+            ok = __shfl_sync(FULL, ok, 0);
+        }
+    } else if (warp == kEpiWarps + 1) {  // products
+        int i = 0, acc = 0;
+        bool ok = true;
+        for (int id = first; ok && find_tile(p, cur, id, t); id += step) {
+            const int subs = subs_of(p, t);
+            const uint32_t idesc = tc::instr_desc(F8, 128, (t.rows + 15) / 16 * 16);
+            if (lane == 0) {
+                for (int k = k_lo; k < k_hi; ++k, ++i) {
+                    if (F8 || k == k_lo) {
+                        if (acc >= 2 && !tc::bar_wait(acc_empty(acc & 1), (acc / 2 - 1) & 1, stop)) {
+                            ok = false;
+                            break;
+                        }
+                    }
+                    const int s = i % p.stages;
+                    if (!tc::bar_wait(full(s), (i / p.stages) & 1, stop)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after();
+                    const uint32_t at = ring + s * sb;
+                    const uint64_t b = tc::smem_desc(at + p.na * kSub);
+                    for (int a = 0; a < subs; ++a) {
+                        const uint64_t w = tc::smem_desc(at + a * kSub);
+                        const uint32_t d = tmem + ((acc & 1) * p.na + a) * p.bn;
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, o));
-                if (live && tx == 0) p.out_scale[row * nb + blockIdx.x] = amax / 448.0f;
+                        for (int q = 0; q < 4; ++q)  // 32 bytes of K each
+                            tc::mma<F8>(d, w + 2 * q, b + 2 * q, idesc, (q > 0 || (!F8 && k > k_lo)) ? 1u : 0u);
+                    }
+                    tc::commit(empty(s));
+                    if (F8 || k == k_hi - 1) {
+                        tc::commit(acc_full(acc & 1));
+                        ++acc;
+                    }
+                }
+                if (!ok) {
+                    tc::commit(drained);
+                    tc::bar_drain(drained, 0);
+                }
             }
+            ok = __shfl_sync(FULL, ok, 0);
+        }
+    } else if (warp == kEpiWarps + 2) {  // e4m3: row scale x weight block scale of each block and column
+        if (F8) {
+            int acc = 0;
+            bool ok = true;
+            const int nb = (p.N + 127) / 128;
+            for (int id = first; ok && find_tile(p, cur, id, t); id += step) {
+                const int subs = subs_of(p, t);
+                const float* ws[2];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int n = n0 + tx + 32 * j;
-                if (!live || n >= p.N) continue;
-                const int64_t at = row * p.N + n;
-                if (p.out_type == EP_DTYPE_E4M3)
-                    static_cast<uint8_t*>(p.out)[at] = (uint8_t)(pack_e4m3x2(v[j] * (448.0f / amax), 0.f) & 0xff);
-                else if (p.out_type == EP_DTYPE_FP32)
-                    static_cast<float*>(p.out)[at] = v[j];
-                else
-                    static_cast<uint16_t*>(p.out)[at] = (uint16_t)(pack_bf16x2(v[j], 0.f) & 0xffff);
+                for (int a = 0; a < 2; ++a)
+                    ws[a] = p.w_scale + ((int64_t)(t.group / p.R * p.parts + (p.parts == 2 ? a : 0)) * nb +
+                                         min(channel_of(p, t, a) / 128, nb - 1)) * p.kblocks;
+                for (int k = k_lo; ok && k < k_hi; ++k, ++acc) {
+                    float xs[kMaxBn / 32];
+#pragma unroll
+                    for (int j = 0; j < kMaxBn / 32; ++j)
+                        xs[j] = lane + 32 * j < t.rows ? p.x_scale[(t.row + lane + 32 * j) * p.kblocks + k] : 0.f;
+                    const float w0 = ws[0][k], w1 = subs == 2 ? ws[1][k] : 0.f;
+                    if (acc >= 2) ok = tc::bar_wait(acc_empty(acc & 1), (acc / 2 - 1) & 1, stop);
+                    ok = __all_sync(FULL, ok);
+                    if (!ok) break;
+                    float* dst = scales + (acc & 1) * 2 * kMaxBn;
+#pragma unroll
+                    for (int j = 0; j < kMaxBn / 32; ++j)
+                        if (32 * j < p.bn) {
+                            dst[lane + 32 * j] = xs[j] * w0;
+                            dst[kMaxBn + lane + 32 * j] = xs[j] * w1;
+                        }
+                    tc::bar_arrive(scale_full(acc & 1));
+                }
+            }
+        }
+    } else {  // epilogue: warps 0-3 read sub-tile 0, warps 4-7 sub-tile 1
+        const int sub = warp >> 2;
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        const int col = sub * 128 + (warp & 3) * 32 + lane;  // channel within a staged row
+        int acc = 0;
+        bool ok = true;
+        for (int id = first; ok && find_tile(p, cur, id, t); id += step) {
+            const int subs = subs_of(p, t);
+            Bias bias;
+            load_bias(p, t, subs, bias);
+            uint64_t sum[F8 ? kMaxBn / 2 : 1];  // fp32 pairs: columns 2i, 2i + 1
+            if (F8) {
+#pragma unroll
+                for (int i = 0; i < kMaxBn / 2; ++i) sum[i] = 0;
+                for (int k = k_lo; ok && k < k_hi; ++k, ++acc) {
+                    ok = tc::bar_wait(acc_full(acc & 1), (acc / 2) & 1, stop) &&
+                         tc::bar_wait(scale_full(acc & 1), (acc / 2) & 1, stop);
+                    ok = __all_sync(FULL, ok);
+                    if (!ok) break;
+                    tc::fence_after();
+                    if (sub < subs) {
+                        const ulonglong2* sc = reinterpret_cast<const ulonglong2*>(scales + ((acc & 1) * 2 + sub) * kMaxBn);
+                        const uint32_t at = tmem + lane_base + ((acc & 1) * p.na + sub) * p.bn;
+#pragma unroll
+                        for (int c = 0; c < kMaxBn / 32; ++c) {
+                            if (c * 32 >= t.rows) continue;
+                            uint32_t v[32];
+                            tc::tmem_ld32(at + c * 32, v);
+                            tc::tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const ulonglong2 s2 = sc[c * 8 + j];
+                                sum[c * 16 + 2 * j] = f32x2_fma_rn(
+                                    f32x2_pack(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1])), s2.x,
+                                    sum[c * 16 + 2 * j]);
+                                sum[c * 16 + 2 * j + 1] = f32x2_fma_rn(
+                                    f32x2_pack(__uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3])), s2.y,
+                                    sum[c * 16 + 2 * j + 1]);
+                            }
+                        }
+                    }
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::bar_arrive(acc_empty(acc & 1));
+                }
+            } else {
+                ok = __all_sync(FULL, tc::bar_wait(acc_full(acc & 1), (acc / 2) & 1, stop));
+                tc::fence_after();
+            }
+            // all warps leave after the same tile: none may wait below for one that left
+            ok = epi_sync_and(ok);
+            const uint32_t at = tmem + lane_base + ((acc & 1) * p.na + sub) * p.bn;
+            const int width = subs * 128;
+#pragma unroll
+            for (int c = 0; c < kMaxBn / 32; ++c) {
+                if (c * 32 >= t.rows) continue;
+                if (!SPLIT && c > 0) epi_sync();  // staging is free
+                float* row0 = staging + (SPLIT ? c * 32 * width : 0) + col;
+                if (ok && sub < subs) {
+                    if (F8) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float2 v = f32x2_unpack(sum[F8 ? c * 16 + j : 0]);
+                            row0[(2 * j) * width] = v.x;
+                            row0[(2 * j + 1) * width] = v.y;
+                        }
+                    } else {
+                        uint32_t v[32];
+                        tc::tmem_ld32(at + c * 32, v);
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) row0[j * width] = __uint_as_float(v[j]);
+                    }
+                }
+                if (!SPLIT) {
+                    epi_sync();
+                    if (ok)
+                        for (int r = warp; r < 32 && c * 32 + r < t.rows; r += kEpiWarps)
+                            emit_row(p, t, subs, bias, t.row + c * 32 + r, [&](int s) {
+                                return *reinterpret_cast<const float4*>(staging + r * width + s * 128 + lane * 4);
+                            });
+                }
+            }
+            if (!F8) {
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) tc::bar_arrive(acc_empty(acc & 1));
+                ++acc;
             }
         }
     }
+    if (SPLIT) {
+        // every CTA of the cluster holds its part of the tile's sums in
+        // staging (its products, and so its ring, are done); rows go round
+        __syncwarp();
+        tc::cluster_sync();
+        Cursor c2;
+        if (!*stop && warp < kEpiWarps && find_tile(p, c2, first, t)) {
+            const int subs = subs_of(p, t), width = subs * 128;
+            Bias bias;
+            load_bias(p, t, subs, bias);
+            const uint32_t mine = tc::smem_u32(staging);
+            for (int r = rank + warp * p.splits; r < t.rows; r += kEpiWarps * p.splits)
+                emit_row(p, t, subs, bias, t.row + r, [&](int s) {
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int q = 0; q < p.splits; ++q) {
+                        const float4 w = tc::ld_peer(tc::peer_smem(mine + (r * width + s * 128 + lane * 4) * 4, q));
+                        v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+                    }
+                    return v;
+                });
+        }
+        __syncwarp();
+        tc::cluster_sync();
+    } else {
+        __syncwarp();
+        __syncthreads();
+    }
+    if (threadIdx.x == 0 && *stop) set_error(p.err, EP_DEVERR_TIMEOUT);
+    if (warp == kEpiWarps + 1) tc::tmem_free(tmem, p.cols);
+}
+
+// ---- host ----------------------------------------------------------------------
+
+using encode_t = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// cuTensorMapEncodeTiled through the runtime (libep links no libcuda); NULL if the driver lacks it.
+encode_t encoder() {
+    static const encode_t f = [] {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            fn = nullptr;
+        return reinterpret_cast<encode_t>(fn);
+    }();
+    return f;
+}
+
+// A row-major array as tiles of 128 bytes x box_rows, 128-byte swizzled, zeros outside.
+bool encode(CUtensorMap* map, bool f8, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+            int box_rows) {
+    const cuuint32_t box[4] = {f8 ? 128u : 64u, (cuuint32_t)box_rows, 1, 1}, one[4] = {1, 1, 1, 1};
+    return encoder()(map, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
+                     const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 ep_status_t check_linear(const ep_linear_t* q, int64_t rows) {
@@ -201,26 +588,81 @@ LinearParams params_of(const ep_linear_t& q) {
     return p;
 }
 
-// avg: rows per group to expect (any count is right).
-ep_status_t launch(const ep_buffer& b, const LinearParams& p, int64_t avg, void* stream) {
+// Chooses tile, split and grid and launches. x_rows: rows that x holds;
+// weights: matrices in w; avg: rows of a group to expect (any count is right).
+ep_status_t launch_on_device(const ep_buffer& b, LinearParams p, int64_t x_rows, int weights, int64_t avg, int64_t most,
+                             cudaStream_t stream) {
+    const bool f8 = p.x_scale != nullptr;
+    const int size = f8 ? 1 : 2;
+    p.kblocks = f8 ? p.K / 128 : (p.K + 63) / 64;
+    p.bn = avg <= 32 ? 32 : avg <= 64 ? 64 : 128;
+    p.vec = p.N % 4 == 0;
+    // row tiles there can be, and that are likely
+    const int64_t groups = most < p.G ? most : p.G;
+    const int64_t bound = (p.cnt ? (int64_t)p.G * ((p.region + p.bn - 1) / p.bn) : most / p.bn + groups);
+    const int64_t likely = groups * ((avg + p.bn - 1) / p.bn);
+    // two weight tiles per CTA share its rows of x; one where tiles are few
+    p.na = 2;
+    p.nt = p.parts == 2 ? (p.N + 127) / 128 : (p.N + 255) / 256;
+    if (p.parts == 1 && (p.N <= 128 || likely * p.nt < b.sm_count)) {
+        p.na = 1;
+        p.nt = (p.N + 127) / 128;
+    }
+    if (bound * p.nt >= (int64_t)1 << 30) return fail(EP_ERR_UNSUPPORTED, "too many tiles: rows x out_features");
+    p.splits = 1;
+    while (p.splits < 8 && 2 * p.splits * likely * p.nt <= b.sm_count && p.kblocks >= 4 * p.splits &&
+           bound * p.nt * 2 * p.splits <= 4 * b.sm_count)
+        p.splits *= 2;
+    const bool split = p.splits > 1;
+    const int sb = stage_bytes(p.na, p.bn);
+    const int fixed = kControl + (split ? 0 : kStaging) + 1024;  // 1024: alignment of the ring
+    p.stages = (kSmemMax - fixed) / sb;
+    if (p.stages > kMaxStages) p.stages = kMaxStages;
+    // a split CTA stages its whole tile in the ring
+    const int smem = p.stages * sb + fixed;
+    p.cols = 32;
+    while ((int)p.cols < 2 * p.na * p.bn) p.cols *= 2;
+
+    CUtensorMap map_x, map_w;
+    const cuuint64_t K = p.K, N = p.N;
+    const cuuint64_t dx[2] = {K, (cuuint64_t)x_rows}, sx[1] = {K * size};
+    const cuuint64_t dw[4] = {K, N, (cuuint64_t)p.parts, (cuuint64_t)weights},
+                     sw[3] = {K * size, N * K * size, (cuuint64_t)p.wide * K * size};
+    if (!encoder()) return fail(EP_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled");
+    if (!encode(&map_x, f8, p.x, 2, dx, sx, p.bn) || !encode(&map_w, f8, p.w, 4, dw, sw, 128))
+        return fail(EP_ERR_UNSUPPORTED, "x or w is too large for a tensor map");
+
+    auto kernel = split ? (f8 ? linear_kernel<true, true> : linear_kernel<false, true>)
+                        : (f8 ? linear_kernel<true, false> : linear_kernel<false, false>);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+    if (e != cudaSuccess) return fail(EP_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    const int64_t tiles = bound * p.nt;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(split ? tiles * p.splits : tiles < b.sm_count ? tiles : b.sm_count));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.splits;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, map_x, map_w, p);
+    if (e != cudaSuccess) return fail(EP_ERR_CUDA, "linear launch: %s", cudaGetErrorString(e));
+    set_last_error("");
+    return EP_OK;
+}
+
+ep_status_t launch(const ep_buffer& b, const LinearParams& p, int64_t x_rows, int weights, int64_t avg, int64_t most,
+                   void* stream) {
     int prev = 0;
     cudaError_t e = cudaGetDevice(&prev);
     if (e == cudaSuccess && prev != b.device) e = cudaSetDevice(b.device);
     if (e != cudaSuccess) return fail(EP_ERR_CUDA, "cudaSetDevice: %s", cudaGetErrorString(e));
-    int64_t rt = (avg + kTile - 1) / kTile;
-    if (rt < 1) rt = 1;
-    if (rt > 65535) rt = 65535;
-    const int gmax = 65535;
-    e = cudaSuccess;
-    if (p.G > gmax) e = cudaErrorInvalidValue;
-    if (e == cudaSuccess) {
-        linear_kernel<<<dim3((p.N + 127) / 128, (unsigned)rt, (unsigned)p.G), 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
-        e = cudaGetLastError();
-    }
+    const ep_status_t st = launch_on_device(b, p, x_rows, weights, avg, most, static_cast<cudaStream_t>(stream));
     if (prev != b.device) cudaSetDevice(prev);
-    if (e != cudaSuccess) return fail(EP_ERR_CUDA, "linear launch: %s", cudaGetErrorString(e));
-    set_last_error("");
-    return EP_OK;
+    return st;
 }
 
 }  // namespace
@@ -240,7 +682,7 @@ ep_status_t ep_linear(ep_buffer_t* b, int64_t rows, const ep_linear_t* q, void* 
     p.G = 1;
     p.rows = p.row_limit = rows;
     p.err = b->err;
-    return launch(*b, p, rows, stream);
+    return launch(*b, p, rows, 1, rows, rows, stream);
 }
 
 ep_status_t ep_expert_linear(ep_buffer_t* b, int T, const ep_linear_t* q, void* stream) {
@@ -266,8 +708,8 @@ ep_status_t ep_expert_linear(ep_buffer_t* b, int T, const ep_linear_t* q, void* 
         p.G = sh ? E / R : E;
         p.off = sh ? b->recv_off : b->expert_off;
     }
-    const int64_t avg = (int64_t)R * T * b->cfg.topk / (sh ? E : p.G) + 1;
-    return launch(*b, p, avg, stream);
+    const int64_t avg = (rows + (sh ? E : p.G) - 1) / (sh ? E : p.G);
+    return launch(*b, p, p.row_limit, sh ? E / R : E, avg, rows, stream);
 }
 
 }  // extern "C"
