@@ -290,73 +290,78 @@ __global__ void __launch_bounds__(kThreads, 1)
     Cursor cur;
     Tile t;
 
+    // The loads and products warps run their loops whole and converged; one
+    // elected lane issues.
     if (warp == kEpiWarps) {  // loads
-        int i = 0;
+        int i = 0, s = 0;
+        uint32_t wrap = 0;
         bool ok = true;
         for (int id = first; ok && find_tile(p, cur, id, t); id += step) {
             const int subs = subs_of(p, t);
             const uint32_t bytes = subs * kSub + p.bn * 128;
-            if (lane == 0) {
-                for (int k = k_lo; k < k_hi; ++k, ++i) {
-                    const int s = i % p.stages;
-                    if (i >= p.stages && !tc::bar_wait(empty(s), (i / p.stages - 1) & 1, stop)) {
-                        ok = false;
-                        break;
-                    }
+            for (int k = k_lo; k < k_hi; ++k, ++i) {
+                if (wrap > 0) ok = __all_sync(FULL, tc::bar_wait(empty(s), (wrap - 1) & 1, stop));
+                if (!ok) break;
+                if (tc::elect()) {
                     const uint32_t at = ring + s * sb;
                     tc::bar_expect(full(s), bytes);
-                    for (int a = 0; a < subs; ++a)
-                        tc::tma_4d(at + a * kSub, &map_w, full(s), k * kElems, channel_of(p, t, a), p.parts == 2 ? a : 0,
+                    tc::tma_4d(at, &map_w, full(s), k * kElems, channel_of(p, t, 0), 0, t.group / p.R);
+                    if (subs == 2)
+                        tc::tma_4d(at + kSub, &map_w, full(s), k * kElems, channel_of(p, t, 1), p.parts == 2 ? 1 : 0,
                                    t.group / p.R);
                     tc::tma_2d(at + p.na * kSub, &map_x, full(s), k * kElems, (int)t.row);
                 }
-                if (!ok)  // copies in flight land before the CTA leaves
-                    for (int j = i > p.stages ? i - p.stages : 0; j < i; ++j)
-                        tc::bar_drain(full(j % p.stages), (j / p.stages) & 1);
+                __syncwarp();
+                if (++s == p.stages) {
+                    s = 0;
+                    ++wrap;
+                }
             }
-            ok = __shfl_sync(FULL, ok, 0);
+            if (!ok && lane == 0)  // copies in flight land before the CTA leaves
+                for (int j = i > p.stages ? i - p.stages : 0; j < i; ++j)
+                    tc::bar_drain(full(j % p.stages), (j / p.stages) & 1);
         }
     } else if (warp == kEpiWarps + 1) {  // products
-        int i = 0, acc = 0;
+        int s = 0, acc = 0;
+        uint32_t wrap = 0;
         bool ok = true;
         for (int id = first; ok && find_tile(p, cur, id, t); id += step) {
             const int subs = subs_of(p, t);
             const uint32_t idesc = tc::instr_desc(F8, 128, (t.rows + 15) / 16 * 16);
-            if (lane == 0) {
-                for (int k = k_lo; k < k_hi; ++k, ++i) {
-                    if (F8 || k == k_lo) {
-                        if (acc >= 2 && !tc::bar_wait(acc_empty(acc & 1), (acc / 2 - 1) & 1, stop)) {
-                            ok = false;
-                            break;
-                        }
-                    }
-                    const int s = i % p.stages;
-                    if (!tc::bar_wait(full(s), (i / p.stages) & 1, stop)) {
-                        ok = false;
-                        break;
-                    }
-                    tc::fence_after();
-                    const uint32_t at = ring + s * sb;
-                    const uint64_t b = tc::smem_desc(at + p.na * kSub);
-                    for (int a = 0; a < subs; ++a) {
-                        const uint64_t w = tc::smem_desc(at + a * kSub);
-                        const uint32_t d = tmem + ((acc & 1) * p.na + a) * p.bn;
+            for (int k = k_lo; k < k_hi; ++k) {
+                if ((F8 || k == k_lo) && acc >= 2)
+                    ok = __all_sync(FULL, tc::bar_wait(acc_empty(acc & 1), (acc / 2 - 1) & 1, stop));
+                if (ok) ok = __all_sync(FULL, tc::bar_wait(full(s), wrap & 1, stop));
+                if (!ok) break;
+                tc::fence_after();
+                const uint32_t at = ring + s * sb;
+                const uint64_t b = tc::smem_desc(at + p.na * kSub), w = tc::smem_desc(at);
+                const uint32_t d = tmem + (acc & 1) * p.na * p.bn;
+                const uint32_t keep = !F8 && k > k_lo ? 1u : 0u;
+                const bool last = F8 || k == k_hi - 1;
+                if (tc::elect()) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)  // 32 bytes of K each
-                            tc::mma<F8>(d, w + 2 * q, b + 2 * q, idesc, (q > 0 || (!F8 && k > k_lo)) ? 1u : 0u);
+                    for (int q = 0; q < 4; ++q)  // 32 bytes of K each
+                        tc::mma<F8>(d, w + 2 * q, b + 2 * q, idesc, q > 0 ? 1u : keep);
+                    if (subs == 2) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            tc::mma<F8>(d + p.bn, w + kSub / 16 + 2 * q, b + 2 * q, idesc, q > 0 ? 1u : keep);
                     }
                     tc::commit(empty(s));
-                    if (F8 || k == k_hi - 1) {
-                        tc::commit(acc_full(acc & 1));
-                        ++acc;
-                    }
+                    if (last) tc::commit(acc_full(acc & 1));
                 }
-                if (!ok) {
-                    tc::commit(drained);
-                    tc::bar_drain(drained, 0);
+                __syncwarp();
+                acc += last;
+                if (++s == p.stages) {
+                    s = 0;
+                    ++wrap;
                 }
             }
-            ok = __shfl_sync(FULL, ok, 0);
+            if (!ok) {  // products in flight end before the CTA leaves
+                if (tc::elect()) tc::commit(drained);
+                tc::bar_drain(drained, 0);
+            }
         }
     } else if (warp == kEpiWarps + 2) {  // e4m3: row scale x weight block scale of each block and column
         if (F8) {

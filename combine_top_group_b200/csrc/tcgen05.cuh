@@ -15,6 +15,15 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// True in one lane of a converged warp. The branch on it is one that the
+// compiler knows to hold a single thread, so that what the branch issues can
+// stay in uniform registers.
+__device__ __forceinline__ bool elect() {
+    uint32_t r;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+    return r != 0;
+}
+
 // ---- mbarriers ---------------------------------------------------------------
 
 __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
@@ -34,14 +43,17 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
                  : "memory");
     return ok != 0;
 }
-// Waits for the phase with this parity; false after kWaitLimitNs, or once
+// A wait gives up after this many SM cycles, 2 s at the highest clock.
+constexpr long long kWaitLimitCycles = 4000000000ll;
+
+// Waits for the phase with this parity; false after the limit, or once
 // another thread of the CTA has given up (*stop).
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* stop) {
     if (bar_try(bar, parity)) return true;
-    const unsigned long long t0 = globaltimer_ns();
+    const long long t0 = clock64();
     while (!bar_try(bar, parity)) {
         if (*stop) return false;
-        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        if (clock64() - t0 > kWaitLimitCycles) {
             *stop = 1;
             return false;
         }
@@ -50,9 +62,9 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
 }
 // The same without the stop flag, for draining what a stopped CTA has in flight.
 __device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity) {
-    const unsigned long long t0 = globaltimer_ns();
+    const long long t0 = clock64();
     while (!bar_try(bar, parity))
-        if (globaltimer_ns() - t0 > kWaitLimitNs) return;
+        if (clock64() - t0 > kWaitLimitCycles) return;
 }
 
 // ---- TMA ---------------------------------------------------------------------

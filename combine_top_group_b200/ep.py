@@ -436,43 +436,60 @@ def ep_shard_combine(buf: EpBuffer, rank: int, T: int, peer_y, peer_y_scale, out
 # These take torch tensors only, and check what a pointer cannot say: device,
 # element type, shape and contiguity.
 
+_BF16, _F32, _I32, _U8 = (torch.bfloat16,), (torch.float32,), (torch.int32,), (torch.uint8,)
 _E4M3 = (torch.float8_e4m3fn, torch.uint8)
+_GAMMA = (torch.bfloat16, torch.float32)
+_OUT = (torch.bfloat16, torch.float32, *_E4M3)
+_WORD = (torch.int32, torch.uint32)
 
 
-def _tensor(where: str, name: str, t, dtypes, shape, device) -> None:
-    """t is None, or a contiguous tensor of one of `dtypes` on `device` whose
-    shape is `shape` (the first dimension may hold more if it is (">=", n))."""
-    if t is None:
-        return
-    dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
-    why = None
+def _refuse(where: str, why: str):
+    raise EpError(EP_ERR_INVALID, where, why)
+
+
+def _shape_of(where: str, name: str, t, dims: int):
+    if not isinstance(t, torch.Tensor) or t.dim() != dims:
+        _refuse(where, f"{name} is no tensor of {dims} dimension{'s' if dims > 1 else ''}")
+    return t.shape
+
+
+def _why_not(t, dtypes, dev: int, shape) -> str:
     if not isinstance(t, torch.Tensor):
-        why = "is no tensor"
-    elif t.dtype not in dtypes:
-        why = f"has dtype {t.dtype}, not {' or '.join(str(d) for d in dtypes)}"
-    elif t.device != device or t.device.type != "cuda":
-        why = f"is on {t.device}, not on the CUDA device of the call ({device})"
-    elif not t.is_contiguous():
-        why = "is not contiguous"
-    elif shape is not None:
-        least = isinstance(shape[0], tuple)
-        want = (shape[0][1], *shape[1:]) if least else tuple(shape)
-        ok = t.dim() == len(want) and tuple(t.shape[1:]) == want[1:] and \
-            (t.shape[0] >= want[0] if least else t.shape[0] == want[0])
-        if not ok:
-            why = f"has shape {tuple(t.shape)}, not {'at least ' if least else ''}{want}"
-    if why:
-        raise EpError(EP_ERR_INVALID, where, f"{name} {why}")
+        return "is no tensor"
+    if t.dtype not in dtypes:
+        return f"has dtype {t.dtype}, not {' or '.join(str(d) for d in dtypes)}"
+    if t.get_device() != dev or not t.is_cuda:
+        return f"is on {t.device}, not on the CUDA device of the call"
+    if not t.is_contiguous():
+        return "is not contiguous"
+    return f"has shape {tuple(t.shape)}, not {tuple(shape)}"
 
 
-def _required(where: str, **tensors) -> None:
-    for name, t in tensors.items():
-        if not isinstance(t, torch.Tensor):
-            raise EpError(EP_ERR_INVALID, where, f"{name} is no tensor")
+def _checked(where: str, dev: int, *wanted) -> None:
+    """Each of `wanted` is (name, tensor or None, dtypes, shape or None). A
+    tensor is contiguous, on CUDA device `dev`, and of that type and shape."""
+    for name, t, dtypes, shape in wanted:
+        if t is not None and not (isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == dev and
+                                  t.dtype in dtypes and t.is_contiguous() and (shape is None or t.shape == shape)):
+            _refuse(where, f"{name} {_why_not(t, dtypes, dev, shape if shape is not None else ())}")
 
 
-def _stream_on(device, stream):
-    return torch.cuda.current_stream(device).cuda_stream if stream is None else _stream(stream)
+def _required(where: str, *named) -> None:
+    for name, t in named:
+        if t is None:
+            _refuse(where, f"{name} is None")
+
+
+def _on(dev: int, fn, *args):
+    """fn(*args) with `dev` the current device."""
+    if torch._C._cuda_getDevice() == dev:
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
+
+
+def _stream_on(dev: int, stream):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def ep_rmsnorm_backward_workspace_bytes(N: int, H: int) -> int:
@@ -486,39 +503,31 @@ def ep_rmsnorm(x, gamma, eps: float, residual=None, h=None, y=None, q=None, q_sc
     """Residual addition, RMS norm and e4m3 cast of x [N, H] into whichever
     of h, y, q + q_scale and rstd are given."""
     w = "ep_rmsnorm"
-    _required(w, x=x, gamma=gamma)
-    _tensor(w, "x", x, torch.bfloat16, None, x.device)
-    if x.dim() != 2:
-        raise EpError(EP_ERR_INVALID, w, "x is not [N, H]")
-    N, H = x.shape
-    for name, t, dt, shape in (("gamma", gamma, (torch.bfloat16, torch.float32), (H,)),
-                               ("residual", residual, torch.bfloat16, (N, H)), ("h", h, torch.bfloat16, (N, H)),
-                               ("y", y, torch.bfloat16, (N, H)), ("q", q, _E4M3, (N, H)),
-                               ("q_scale", q_scale, torch.float32, (N, H // 128)), ("rstd", rstd, torch.float32, (N,))):
-        _tensor(w, name, t, dt, shape, x.device)
-    with torch.cuda.device(x.device):
-        _check(_lib.ep_rmsnorm(N, H, _ptr(x), _ptr(residual), _ptr(gamma), int(gamma.dtype == torch.float32), eps,
-                               _ptr(h), _ptr(y), _ptr(q), _ptr(q_scale), _ptr(rstd), _stream_on(x.device, stream)), w)
+    shape = _shape_of(w, "x", x, 2)
+    N, H = shape
+    dev = x.get_device()
+    _required(w, ("gamma", gamma))
+    _checked(w, dev, ("x", x, _BF16, None), ("gamma", gamma, _GAMMA, (H,)), ("residual", residual, _BF16, shape),
+             ("h", h, _BF16, shape), ("y", y, _BF16, shape), ("q", q, _E4M3, shape),
+             ("q_scale", q_scale, _F32, (N, H // 128)), ("rstd", rstd, _F32, (N,)))
+    _check(_on(dev, _lib.ep_rmsnorm, N, H, _ptr(x), _ptr(residual), _ptr(gamma), int(gamma.dtype is torch.float32), eps,
+               _ptr(h), _ptr(y), _ptr(q), _ptr(q_scale), _ptr(rstd), _stream_on(dev, stream)), w)
 
 
 def ep_rmsnorm_backward(h, rstd, gamma, dy, dx, dgamma, workspace, dh=None, stream=None) -> None:
     """Gradient of ep_rmsnorm; workspace: uint8, ep_rmsnorm_backward_workspace_bytes(N, H)."""
     w = "ep_rmsnorm_backward"
-    _required(w, h=h, rstd=rstd, gamma=gamma, dy=dy, dx=dx, dgamma=dgamma, workspace=workspace)
-    _tensor(w, "h", h, torch.bfloat16, None, h.device)
-    if h.dim() != 2:
-        raise EpError(EP_ERR_INVALID, w, "h is not [N, H]")
-    N, H = h.shape
-    for name, t, dt, shape in (("rstd", rstd, torch.float32, (N,)),
-                               ("gamma", gamma, (torch.bfloat16, torch.float32), (H,)),
-                               ("dy", dy, torch.bfloat16, (N, H)), ("dh", dh, torch.bfloat16, (N, H)),
-                               ("dx", dx, torch.bfloat16, (N, H)), ("dgamma", dgamma, torch.float32, (H,)),
-                               ("workspace", workspace, torch.uint8, None)):
-        _tensor(w, name, t, dt, shape, h.device)
-    with torch.cuda.device(h.device):
-        _check(_lib.ep_rmsnorm_backward(N, H, _ptr(h), _ptr(rstd), _ptr(gamma), int(gamma.dtype == torch.float32),
-                                        _ptr(dy), _ptr(dh), _ptr(dx), _ptr(dgamma), _ptr(workspace),
-                                        workspace.numel(), _stream_on(h.device, stream)), w)
+    shape = _shape_of(w, "h", h, 2)
+    N, H = shape
+    dev = h.get_device()
+    _required(w, ("rstd", rstd), ("gamma", gamma), ("dy", dy), ("dx", dx), ("dgamma", dgamma),
+              ("workspace", workspace))
+    _checked(w, dev, ("h", h, _BF16, None), ("rstd", rstd, _F32, (N,)), ("gamma", gamma, _GAMMA, (H,)),
+             ("dy", dy, _BF16, shape), ("dh", dh, _BF16, shape), ("dx", dx, _BF16, shape),
+             ("dgamma", dgamma, _F32, (H,)), ("workspace", workspace, _U8, None))
+    _check(_on(dev, _lib.ep_rmsnorm_backward, N, H, _ptr(h), _ptr(rstd), _ptr(gamma), int(gamma.dtype is torch.float32),
+               _ptr(dy), _ptr(dh), _ptr(dx), _ptr(dgamma), _ptr(workspace), workspace.numel(),
+               _stream_on(dev, stream)), w)
 
 
 def ep_balance_loss_workspace_bytes(N: int, E: int, S: int = 1) -> int:
@@ -527,13 +536,13 @@ def ep_balance_loss_workspace_bytes(N: int, E: int, S: int = 1) -> int:
     return n.value
 
 
-def _sequences(where, seq_off, device) -> int:
+def _sequences(where: str, seq_off) -> int:
     if seq_off is None:
         return 1
-    _tensor(where, "seq_off", seq_off, torch.int32, None, device)
-    if seq_off.dim() != 1 or seq_off.numel() < 2:
-        raise EpError(EP_ERR_INVALID, where, "seq_off is not [S + 1] with S >= 1")
-    return seq_off.numel() - 1
+    n = _shape_of(where, "seq_off", seq_off, 1)[0]
+    if n < 2:
+        _refuse(where, "seq_off is not [S + 1] with S >= 1")
+    return n - 1
 
 
 def ep_balance_loss(logits, topk_idx, score: int, coef: float, loss, counts, workspace, error_word, seq_off=None,
@@ -541,86 +550,77 @@ def ep_balance_loss(logits, topk_idx, score: int, coef: float, loss, counts, wor
     """Balance loss of logits [N, E] and topk_idx [N, K] over the sequences of
     seq_off [S + 1] (None: one); fills loss [1], counts [S, E], prob [S, E]."""
     w = "ep_balance_loss"
-    _required(w, logits=logits, topk_idx=topk_idx, loss=loss, counts=counts, workspace=workspace,
-              error_word=error_word)
-    if logits.dim() != 2 or topk_idx.dim() != 2:
-        raise EpError(EP_ERR_INVALID, w, "logits is not [N, E], or topk_idx not [N, K]")
-    dev = logits.device
-    (N, E), K, S = logits.shape, topk_idx.shape[1], _sequences(w, seq_off, dev)
-    for name, t, dt, shape in (("logits", logits, torch.float32, (N, E)), ("topk_idx", topk_idx, torch.int32, (N, K)),
-                               ("loss", loss, torch.float32, (1,)), ("counts", counts, torch.int32, (S, E)),
-                               ("prob", prob, torch.float32, (S, E)), ("workspace", workspace, torch.uint8, None),
-                               ("error_word", error_word, (torch.int32, torch.uint32), (1,))):
-        _tensor(w, name, t, dt, shape, dev)
-    with torch.cuda.device(dev):
-        _check(_lib.ep_balance_loss(N, E, K, score, _ptr(logits), _ptr(topk_idx), S, _ptr(seq_off), coef, _ptr(loss),
-                                    _ptr(counts), _ptr(prob), _ptr(workspace), workspace.numel(), _ptr(error_word),
-                                    _stream_on(dev, stream)), w)
+    N, E = _shape_of(w, "logits", logits, 2)
+    K, S, dev = _shape_of(w, "topk_idx", topk_idx, 2)[1], _sequences(w, seq_off), logits.get_device()
+    _required(w, ("loss", loss), ("counts", counts), ("workspace", workspace), ("error_word", error_word))
+    _checked(w, dev, ("logits", logits, _F32, None), ("topk_idx", topk_idx, _I32, (N, K)),
+             ("seq_off", seq_off, _I32, None), ("loss", loss, _F32, (1,)), ("counts", counts, _I32, (S, E)),
+             ("prob", prob, _F32, (S, E)), ("workspace", workspace, _U8, None),
+             ("error_word", error_word, _WORD, (1,)))
+    _check(_on(dev, _lib.ep_balance_loss, N, E, K, score, _ptr(logits), _ptr(topk_idx), S, _ptr(seq_off), coef,
+               _ptr(loss), _ptr(counts), _ptr(prob), _ptr(workspace), workspace.numel(), _ptr(error_word),
+               _stream_on(dev, stream)), w)
 
 
 def ep_balance_loss_backward(logits, counts, topk: int, score: int, coef: float, dlogits, seq_off=None,
                              grad_loss=None, accumulate: bool = False, stream=None) -> None:
     """Gradient of ep_balance_loss for the logits, into (or added to) dlogits."""
     w = "ep_balance_loss_backward"
-    _required(w, logits=logits, counts=counts, dlogits=dlogits)
-    if logits.dim() != 2:
-        raise EpError(EP_ERR_INVALID, w, "logits is not [N, E]")
-    dev = logits.device
-    (N, E), S = logits.shape, _sequences(w, seq_off, dev)
-    for name, t, dt, shape in (("logits", logits, torch.float32, (N, E)), ("counts", counts, torch.int32, (S, E)),
-                               ("dlogits", dlogits, torch.float32, (N, E)),
-                               ("grad_loss", grad_loss, torch.float32, (1,))):
-        _tensor(w, name, t, dt, shape, dev)
-    with torch.cuda.device(dev):
-        _check(_lib.ep_balance_loss_backward(N, E, topk, score, _ptr(logits), S, _ptr(seq_off), _ptr(counts), coef,
-                                             _ptr(grad_loss), 1 if accumulate else 0, _ptr(dlogits),
-                                             _stream_on(dev, stream)), w)
+    shape = _shape_of(w, "logits", logits, 2)
+    N, E = shape
+    S, dev = _sequences(w, seq_off), logits.get_device()
+    _required(w, ("counts", counts), ("dlogits", dlogits))
+    _checked(w, dev, ("logits", logits, _F32, None), ("counts", counts, _I32, (S, E)), ("dlogits", dlogits, _F32, shape),
+             ("seq_off", seq_off, _I32, None), ("grad_loss", grad_loss, _F32, (1,)))
+    _check(_on(dev, _lib.ep_balance_loss_backward, N, E, topk, score, _ptr(logits), S, _ptr(seq_off), _ptr(counts), coef,
+               _ptr(grad_loss), 1 if accumulate else 0, _ptr(dlogits), _stream_on(dev, stream)), w)
 
 
-def _linear_args(where, buf, groups, rows, x, w, out, x_scale, w_scale, bias, residual, act, out_scale):
-    """Checks the tensors of a linear layer on `rows` rows (at least) and
+def _linear_args(where, dev, groups, rows, x, w, out, x_scale, w_scale, bias, residual, act, out_scale):
+    """Checks the tensors of a linear layer on at least `rows` rows and
     returns the C struct."""
-    _required(where, x=x, w=w, out=out)
-    dev = buf.workspace.device
-    if x.dim() != 2 or w.dim() != 3 or out.dim() != 2:
-        raise EpError(EP_ERR_INVALID, where, "x, w, out are not [rows, in], [G, wide, in], [rows, out]")
-    cin, cout = x.shape[1], out.shape[1]
-    parts = 2 if act == EP_ACT_SWIGLU else 1
+    have, cin = _shape_of(where, "x", x, 2)
+    room, cout = _shape_of(where, "out", out, 2)
+    _required(where, ("w", w))
     if (x_scale is None) != (w_scale is None):
-        raise EpError(EP_ERR_INVALID, where, "x_scale and w_scale go together")
-    kind = torch.bfloat16 if x_scale is None else _E4M3
-    outs = {torch.bfloat16: EP_DTYPE_BF16, torch.float32: EP_DTYPE_FP32}
-    n = (">=", rows)
-    for name, t, dt, shape in (("x", x, kind, (n, cin)), ("w", w, kind, (groups, parts * cout, cin)),
-                               ("x_scale", x_scale, torch.float32, (n, cin // 128)),
-                               ("w_scale", w_scale, torch.float32, (groups, parts * -(-cout // 128), cin // 128)),
-                               ("bias", bias, torch.float32, (groups, parts * cout)),
-                               ("residual", residual, torch.bfloat16, (n, cout)),
-                               ("out", out, (torch.bfloat16, torch.float32, *_E4M3), (n, cout)),
-                               ("out_scale", out_scale, torch.float32, (n, cout // 128))):
-        _tensor(where, name, t, dt, shape, dev)
-    return EpLinear(x=_ptr(x), x_scale=_ptr(x_scale), w=_ptr(w), w_scale=_ptr(w_scale), bias=_ptr(bias),
-                    residual=_ptr(residual), out=_ptr(out), out_scale=_ptr(out_scale), in_features=cin,
-                    out_features=cout, act=act, out_type=outs.get(out.dtype, EP_DTYPE_E4M3))
+        _refuse(where, "x_scale and w_scale go together")
+    if min(have, room) < rows:
+        _refuse(where, f"x and out hold {have} and {room} rows, the call needs {rows}")
+    for name, t in (("x_scale", x_scale), ("residual", residual), ("out_scale", out_scale)):
+        if t is not None and _shape_of(where, name, t, 2)[0] < rows:
+            _refuse(where, f"{name} holds {t.shape[0]} rows, the call needs {rows}")
+    parts = 2 if act == EP_ACT_SWIGLU else 1
+    kind = _BF16 if x_scale is None else _E4M3
+    _checked(where, dev, ("x", x, kind, None), ("w", w, kind, (groups, parts * cout, cin)), ("out", out, _OUT, None),
+             ("bias", bias, _F32, (groups, parts * cout)))
+    if x_scale is not None:
+        _checked(where, dev, ("x_scale", x_scale, _F32, (x_scale.shape[0], cin // 128)),
+                 ("w_scale", w_scale, _F32, (groups, parts * -(-cout // 128), cin // 128)))
+    if residual is not None:
+        _checked(where, dev, ("residual", residual, _BF16, (residual.shape[0], cout)))
+    if out_scale is not None:
+        _checked(where, dev, ("out_scale", out_scale, _F32, (out_scale.shape[0], cout // 128)))
+    dt = out.dtype
+    return EpLinear(_ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(bias), _ptr(residual), _ptr(out),
+                    _ptr(out_scale), cin, cout, act,
+                    EP_DTYPE_BF16 if dt is torch.bfloat16 else EP_DTYPE_FP32 if dt is torch.float32 else EP_DTYPE_E4M3)
 
 
 def ep_linear(buf: EpBuffer, x, w, out, x_scale=None, w_scale=None, bias=None, residual=None,
               act: int = EP_ACT_NONE, out_scale=None, stream=None) -> None:
     """out = act(x w[0]^T + bias) + residual on x [rows, in]; w [1, wide, in]."""
-    rows = x.shape[0] if isinstance(x, torch.Tensor) and x.dim() == 2 else 0
-    a = _linear_args("ep_linear", buf, 1, rows, x, w, out, x_scale, w_scale, bias, residual, act, out_scale)
-    _check(_lib.ep_linear(buf.handle, rows, ctypes.byref(a), _stream_on(buf.workspace.device, stream)), "ep_linear")
+    rows, dev = _shape_of("ep_linear", "x", x, 2)[0], buf.workspace.get_device()
+    a = _linear_args("ep_linear", dev, 1, rows, x, w, out, x_scale, w_scale, bias, residual, act, out_scale)
+    _check(_lib.ep_linear(buf.handle, rows, ctypes.byref(a), _stream_on(dev, stream)), "ep_linear")
 
 
 def ep_expert_linear(buf: EpBuffer, T: int, x, w, out, x_scale=None, w_scale=None, bias=None, residual=None,
                      act: int = EP_ACT_NONE, out_scale=None, stream=None) -> None:
     """The experts' layer on the receive rows of the last layout: x [rows, in],
     w [experts, wide, in] (a shard's own experts with EP_FLAG_SHARD)."""
-    c = buf.cfg
-    ll = bool(c.flags & EP_FLAG_LOW_LATENCY)
-    rows = c.num_experts * c.num_ranks * c.max_tokens_per_rank if ll else c.num_ranks * T * c.topk
-    groups = c.num_experts // c.num_ranks if buf.shard else c.num_experts
-    a = _linear_args("ep_expert_linear", buf, groups, rows, x, w, out, x_scale, w_scale, bias, residual, act,
-                     out_scale)
-    _check(_lib.ep_expert_linear(buf.handle, T, ctypes.byref(a), _stream_on(buf.workspace.device, stream)),
-           "ep_expert_linear")
+    c, dev = buf.cfg, buf.workspace.get_device()
+    E, R, flags = c.num_experts, c.num_ranks, c.flags
+    rows = E * R * c.max_tokens_per_rank if flags & EP_FLAG_LOW_LATENCY else R * T * c.topk
+    a = _linear_args("ep_expert_linear", dev, E // R if flags & EP_FLAG_SHARD else E, rows, x, w, out, x_scale, w_scale,
+                     bias, residual, act, out_scale)
+    _check(_lib.ep_expert_linear(buf.handle, T, ctypes.byref(a), _stream_on(dev, stream)), "ep_expert_linear")
