@@ -169,9 +169,16 @@ __device__ __forceinline__ void load_bias(const LinearParams& p, const Tile& t, 
 __device__ __forceinline__ void emit(const LinearParams& p, int64_t row, int n, float (&z)[4], const float (&u)[4]) {
     const int lane = threadIdx.x & 31;
     n += lane * 4;
+    if (p.act == EP_ACT_SWIGLU) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        z[i] = p.act == EP_ACT_SWIGLU ? activate(EP_ACT_SILU, z[i]) * u[i] : activate(p.act, z[i]);
+        for (int i = 0; i < 4; ++i) z[i] = activate(EP_ACT_SILU, z[i]) * u[i];
+    } else if (p.act == EP_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] = activate(EP_ACT_SILU, z[i]);
+    } else if (p.act == EP_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] = activate(EP_ACT_GELU, z[i]);
+    }
     const int64_t at = row * p.N + n;
     if (p.vec) {
         if (p.res && n < p.N) {
@@ -517,6 +524,347 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kEpiWarps + 1) tc::tmem_free(tmem, p.cols);
 }
 
+// ---- many rows per group: pairs of CTAs ------------------------------------------
+// The product the other way round, x W^T: 256 rows of x are the lanes (128 in
+// each CTA of the pair), 256 rows of W the columns (gate and up of 128
+// channels, or 256 channels; each CTA loads 128 of them and both use all). A
+// CTA then moves 32 KB into shared memory for 256 x 128 sums of a 64-channel
+// block and the tensor cores read 8 KB per 16 channels, half of what they
+// read for two products of 128 x 128; shared memory is what bounds those. A
+// thread owns a row: its e4m3 scale is one register, and the epilogue needs no
+// exchange but the amax of an e4m3 row between two warps.
+
+// Three warpgroups: two of the epilogue, one of loads, products and two idle
+// warps. The launch gives each thread 168 registers; the epilogue's fp32 sums
+// need more: 2 * 128 * 224 + 128 * 56 = 384 * 168.
+constexpr int kPairThreads = 384;
+constexpr int kEpiRegs = 224, kOtherRegs = 56;
+static_assert(2 * 128 * kEpiRegs + 128 * kOtherRegs == kPairThreads * 168, "register split");
+constexpr int kPairStage = 2 * kSub;
+constexpr int kPairStages = 6;
+constexpr int kPairSmem = kPairStages * kPairStage + 256 + 2 * 128 * 4 + 1024;
+
+// 32 channels from n of a row, rounded and stored.
+__device__ __forceinline__ void store32(const LinearParams& p, int64_t row, int n, const float (&y)[32], float scale) {
+    const int64_t at = row * p.N + n;
+    if (p.out_type == EP_DTYPE_E4M3) {
+        uint4* o = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + at);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float* v = y + 16 * i + 4 * j;
+                w[j] = pack_e4m3x2(v[0] * scale, v[1] * scale) | pack_e4m3x2(v[2] * scale, v[3] * scale) << 16;
+            }
+            o[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        return;
+    }
+    if (p.out_type == EP_DTYPE_FP32) {
+        float* o = static_cast<float*>(p.out) + at;
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+            if (p.N % 4 == 0) {
+                if (n + i < p.N) *reinterpret_cast<float4*>(o + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (n + i + j < p.N) o[i + j] = y[i + j];
+            }
+        }
+        return;
+    }
+    uint16_t* o = static_cast<uint16_t*>(p.out) + at;
+#pragma unroll
+    for (int i = 0; i < 32; i += 8) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(y[i + 2 * j], y[i + 2 * j + 1]);
+        if (p.N % 8 == 0) {
+            if (n + i < p.N) *reinterpret_cast<uint4*>(o + i) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (n + i + j < p.N) o[i + j] = (uint16_t)(w[j / 2] >> 16 * (j & 1));
+        }
+    }
+}
+
+// Bias, activation and residual of 32 channels from n of a row.
+__device__ __forceinline__ void finish32(const LinearParams& p, int g, int64_t row, int n, const float (&z)[32],
+                                         const float (&u)[32], float (&y)[32]) {
+    const float* bias = p.bias ? p.bias + (int64_t)g * p.wide + n : nullptr;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) y[i] = z[i] + (bias && n + i < p.N ? bias[i] : 0.f);
+    // one choice for all channels: a branch for each cost more than the products
+    // of a 2048-channel layer (503 against 1260 TFLOP/s)
+    if (p.act == EP_ACT_SWIGLU) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            y[i] = activate(EP_ACT_SILU, y[i]) * (u[i] + (bias && n + i < p.N ? bias[p.N + i] : 0.f));
+    } else if (p.act == EP_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) y[i] = activate(EP_ACT_SILU, y[i]);
+    } else if (p.act == EP_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) y[i] = activate(EP_ACT_GELU, y[i]);
+    }
+    if (p.res) {
+        const uint16_t* r = p.res + row * p.N + n;
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) {
+            if (p.N % 8 == 0) {
+                if (n + i >= p.N) continue;
+                const uint4 v = *reinterpret_cast<const uint4*>(r + i);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    y[i + 2 * j] += bf16lo(w[j]);
+                    y[i + 2 * j + 1] += bf16hi(w[j]);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (n + i + j < p.N) y[i + j] += __uint_as_float((uint32_t)r[i + j] << 16);
+            }
+        }
+    }
+}
+
+template <bool F8>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    linear_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                       LinearParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t ring = (tc::smem_u32(smem_raw) + 1023) & ~1023u;
+    uint8_t* control = smem_raw + (ring - tc::smem_u32(smem_raw)) + kPairStages * kPairStage;
+    float* row_amax = reinterpret_cast<float*>(control + 256);  // [2][128]
+    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(control + 240);
+    volatile uint32_t* stop = reinterpret_cast<uint32_t*>(control + 244);
+    const uint32_t bars = tc::smem_u32(control);
+    auto full = [&](int s) { return bars + 8 * s; };  // the leader's are used
+    auto empty = [&](int s) { return bars + 8 * (kPairStages + s); };
+    auto acc_full = [&](int s) { return bars + 8 * (2 * kPairStages + s); };
+    auto acc_empty = [&](int s) { return bars + 8 * (2 * kPairStages + 2 + s); };  // the leader's are used
+    const uint32_t drained = bars + 8 * (2 * kPairStages + 4);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)tc::cluster_rank();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kPairStages; ++s) {
+            tc::bar_init(full(s), 1);
+            tc::bar_init(empty(s), 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            tc::bar_init(acc_full(s), 1);
+            tc::bar_init(acc_empty(s), 2 * kEpiWarps);
+        }
+        tc::bar_init(drained, 1);
+        *stop = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kEpiWarps + 1) tc::pair_tmem_alloc(tc::smem_u32(tmem_at), 512);
+    tc::fence_before();
+    __syncthreads();
+    tc::cluster_sync();
+    tc::fence_after();
+    const uint32_t tmem = *tmem_at;
+    const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    constexpr int kElems = F8 ? 128 : 64;
+    Cursor cur;
+    Tile t;
+
+    if (warp == kEpiWarps) {  // loads, each CTA its halves
+        tc::fewer_registers<kOtherRegs>();
+        int i = 0, s = 0;
+        uint32_t wrap = 0;
+        bool ok = true;
+        for (int id = first; ok && find_tile(p, cur, id, t); id += step) {
+            const int ch = p.parts == 2 ? t.n * 128 : t.n * 256 + rank * 128, part = p.parts == 2 ? rank : 0;
+            for (int k = 0; k < p.kblocks; ++k, ++i) {
+                if (wrap > 0) ok = __all_sync(FULL, tc::bar_wait_cluster(empty(s), (wrap - 1) & 1, stop));
+                if (!ok) break;
+                if (tc::elect()) {
+                    const uint32_t at = ring + s * kPairStage, bar = tc::peer_smem(full(s), 0);
+                    if (rank == 0) tc::bar_expect(full(s), 2 * kPairStage);
+                    tc::pair_tma_2d(at, &map_x, bar, k * kElems, (int)t.row + rank * 128);
+                    tc::pair_tma_4d(at + kSub, &map_w, bar, k * kElems, ch, part, t.group / p.R);
+                }
+                __syncwarp();
+                if (++s == kPairStages) {
+                    s = 0;
+                    ++wrap;
+                }
+            }
+            if (!ok && lane == 0 && rank == 0)  // the pair's copies in flight land before it leaves
+                for (int j = i > kPairStages ? i - kPairStages : 0; j < i; ++j)
+                    tc::bar_drain(full(j % kPairStages), (j / kPairStages) & 1);
+        }
+    } else if (warp == kEpiWarps + 1) {  // products, by the leader
+        tc::fewer_registers<kOtherRegs>();
+        if (rank == 0) {
+            int s = 0, acc = 0;
+            uint32_t wrap = 0;
+            bool ok = true;
+            const uint32_t idesc = tc::instr_desc(F8, 256, 256);
+            for (int id = first; ok && find_tile(p, cur, id, t); id += step) {
+                for (int k = 0; k < p.kblocks; ++k) {
+                    if ((F8 || k == 0) && acc >= 2)
+                        ok = __all_sync(FULL, tc::bar_wait_cluster(acc_empty(acc & 1), (acc / 2 - 1) & 1, stop));
+                    if (ok) ok = __all_sync(FULL, tc::bar_wait_cluster(full(s), wrap & 1, stop));
+                    if (!ok) break;
+                    tc::fence_after();
+                    const uint32_t at = ring + s * kPairStage;
+                    const uint64_t a = tc::smem_desc(at), w = tc::smem_desc(at + kSub);
+                    const uint32_t d = tmem + (acc & 1) * 256;
+                    const uint32_t keep = !F8 && k > 0 ? 1u : 0u;
+                    const bool last = F8 || k == p.kblocks - 1;
+                    if (tc::elect()) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)  // 32 bytes of K each
+                            tc::pair_mma<F8>(d, a + 2 * q, w + 2 * q, idesc, q > 0 ? 1u : keep);
+                        tc::pair_commit(empty(s));
+                        if (last) tc::pair_commit(acc_full(acc & 1));
+                    }
+                    __syncwarp();
+                    acc += last;
+                    if (++s == kPairStages) {
+                        s = 0;
+                        ++wrap;
+                    }
+                }
+                if (!ok) {  // products in flight end before the pair leaves
+                    if (tc::elect()) tc::pair_commit(drained);
+                    tc::bar_drain(drained, 0);
+                }
+            }
+        }
+    } else if (warp < kEpiWarps) {  // epilogue: warps w and w + 4 share 32 rows, half of the channels each
+        tc::more_registers<kEpiRegs>();
+        const int half = warp >> 2;
+        const int r = (warp & 3) * 32 + lane;  // row of the CTA's 128
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        const bool gated = p.parts == 2;
+        // column of chunk c: two chunks of gate and two of up, or four neighbours
+        auto column = [&](int c) { return gated ? (c >> 1) * 128 + half * 64 + (c & 1) * 32 : half * 128 + c * 32; };
+        const uint32_t empty_at[2] = {tc::peer_smem(acc_empty(0), 0), tc::peer_smem(acc_empty(1), 0)};
+        int acc = 0;
+        bool ok = true;
+        for (int id = first; ok && find_tile(p, cur, id, t); id += step) {
+            const int rows = min(max(t.rows - rank * 128, 0), 128);  // of this CTA
+            const int64_t row = t.row + rank * 128 + r;
+            const bool live = r < rows;
+            const int g = t.group / p.R;
+            const int n0 = gated ? t.n * 128 + half * 64 : t.n * 256 + half * 128;  // the thread's first channel
+            uint64_t sum[F8 ? 64 : 1];  // fp32 pairs: 32 columns of each chunk
+            if (F8) {
+#pragma unroll
+                for (int i = 0; i < 64; ++i) sum[i] = 0;
+                const int nb = (p.N + 127) / 128;
+                const float* xs = p.x_scale + (live ? row : t.row) * p.kblocks;
+                const float* w0 = p.w_scale + ((int64_t)g * p.parts * nb + (gated ? t.n : min(t.n * 2 + half, nb - 1))) * p.kblocks;
+                const float* w1 = gated ? w0 + (int64_t)nb * p.kblocks : w0;
+                float x_next = xs[0], w0_next = w0[0], w1_next = w1[0];
+                for (int k = 0; ok && k < p.kblocks; ++k, ++acc) {
+                    const float s0 = x_next * w0_next, s1 = x_next * w1_next;
+                    if (k + 1 < p.kblocks) {
+                        x_next = xs[k + 1];
+                        w0_next = w0[k + 1];
+                        w1_next = w1[k + 1];
+                    }
+                    ok = __all_sync(FULL, tc::bar_wait_cluster(acc_full(acc & 1), (acc / 2) & 1, stop));
+                    if (!ok) break;
+                    tc::fence_after();
+                    if (rows > (warp & 3) * 32) {
+                        const uint32_t at = tmem + lane_base + (acc & 1) * 256;
+                        const uint64_t p0 = f32x2_pack(s0, s0), p1 = f32x2_pack(s1, s1);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t v[32];
+                            tc::tmem_ld32(at + column(c), v);
+                            tc::tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                sum[c * 16 + j] =
+                                    f32x2_fma_rn(f32x2_pack(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])),
+                                                 c < 2 ? p0 : p1, sum[c * 16 + j]);
+                        }
+                    }
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::bar_arrive_at(empty_at[acc & 1]);
+                }
+            } else {
+                ok = __all_sync(FULL, tc::bar_wait_cluster(acc_full(acc & 1), (acc / 2) & 1, stop));
+                tc::fence_after();
+            }
+            // all warps leave after the same tile: none may wait below for one that left
+            ok = epi_sync_and(ok);
+            const uint32_t at = tmem + lane_base + (acc & 1) * 256;
+            auto load = [&](int c, float(&z)[32]) {
+                if (F8) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float2 v = f32x2_unpack(sum[F8 ? c * 16 + j : 0]);
+                        z[2 * j] = v.x;
+                        z[2 * j + 1] = v.y;
+                    }
+                } else {
+                    uint32_t v[32];
+                    tc::tmem_ld32(at + column(c), v);
+                    tc::tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) z[j] = __uint_as_float(v[j]);
+                }
+            };
+            const bool e4m3 = p.out_type == EP_DTYPE_E4M3;
+            float amax = 1e-4f;
+            if (ok && rows > (warp & 3) * 32) {
+                // e4m3 goes over the row twice: for its amax, then to store it
+#pragma unroll 1
+                for (int pass = e4m3 ? 0 : 1; pass < 2; ++pass) {
+                    if (pass == 1 && e4m3 && gated) {  // the row's other 64 channels are warp +-4's
+                        row_amax[half * 128 + r] = amax;
+                        asm volatile("bar.sync %0, 64;" ::"r"(2 + (warp & 3)) : "memory");
+                        amax = fmaxf(amax, row_amax[(half ^ 1) * 128 + r]);
+                    }
+                    if (pass == 1 && e4m3 && live && (!gated || half == 0) && n0 < p.N)
+                        p.out_scale[row * (p.N / 128) + n0 / 128] = amax / 448.0f;
+                    const float scale = 448.0f / amax;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        if (c >= (gated ? 2 : 4) || n0 + c * 32 >= p.N) continue;
+                        float z[32], u[32], y[32];
+                        load(c, z);
+                        if (gated) load((c + 2) & 3, u);
+                        if (!live) continue;
+                        finish32(p, g, row, n0 + c * 32, z, u, y);
+                        if (pass == 0) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(y[i]));
+                        } else {
+                            store32(p, row, n0 + c * 32, y, scale);
+                        }
+                    }
+                }
+            }
+            if (!F8) {
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) tc::bar_arrive_at(empty_at[acc & 1]);
+                ++acc;
+            }
+        }
+    } else {
+        tc::fewer_registers<kOtherRegs>();
+    }
+    __syncwarp();
+    __syncthreads();
+    tc::cluster_sync();
+    if (threadIdx.x == 0 && *stop) set_error(p.err, EP_DEVERR_TIMEOUT);
+    if (warp == kEpiWarps + 1) tc::pair_tmem_free(tmem, 512);
+}
+
 // ---- host ----------------------------------------------------------------------
 
 using encode_t = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -593,6 +941,9 @@ LinearParams params_of(const ep_linear_t& q) {
     return p;
 }
 
+// Pairs of CTAs take 256 rows at a time.
+bool use_pair(const LinearParams& p, int64_t avg) { return avg >= 256 && p.wide >= 256; }
+
 // Chooses tile, split and grid and launches. x_rows: rows that x holds;
 // weights: matrices in w; avg: rows of a group to expect (any count is right).
 ep_status_t launch_on_device(const ep_buffer& b, LinearParams p, int64_t x_rows, int weights, int64_t avg, int64_t most,
@@ -600,7 +951,8 @@ ep_status_t launch_on_device(const ep_buffer& b, LinearParams p, int64_t x_rows,
     const bool f8 = p.x_scale != nullptr;
     const int size = f8 ? 1 : 2;
     p.kblocks = f8 ? p.K / 128 : (p.K + 63) / 64;
-    p.bn = avg <= 32 ? 32 : avg <= 64 ? 64 : 128;
+    const bool pair = use_pair(p, avg);
+    p.bn = pair ? 256 : avg <= 32 ? 32 : avg <= 64 ? 64 : 128;
     p.vec = p.N % 4 == 0;
     // row tiles there can be, and that are likely
     const int64_t groups = most < p.G ? most : p.G;
@@ -609,13 +961,13 @@ ep_status_t launch_on_device(const ep_buffer& b, LinearParams p, int64_t x_rows,
     // two weight tiles per CTA share its rows of x; one where tiles are few
     p.na = 2;
     p.nt = p.parts == 2 ? (p.N + 127) / 128 : (p.N + 255) / 256;
-    if (p.parts == 1 && (p.N <= 128 || likely * p.nt < b.sm_count)) {
+    if (!pair && p.parts == 1 && (p.N <= 128 || likely * p.nt < b.sm_count)) {
         p.na = 1;
         p.nt = (p.N + 127) / 128;
     }
     if (bound * p.nt >= (int64_t)1 << 30) return fail(EP_ERR_UNSUPPORTED, "too many tiles: rows x out_features");
     p.splits = 1;
-    while (p.splits < 8 && 2 * p.splits * likely * p.nt <= b.sm_count && p.kblocks >= 4 * p.splits &&
+    while (!pair && p.splits < 8 && 2 * p.splits * likely * p.nt <= b.sm_count && p.kblocks >= 4 * p.splits &&
            bound * p.nt * 2 * p.splits <= 4 * b.sm_count)
         p.splits *= 2;
     const bool split = p.splits > 1;
@@ -634,25 +986,25 @@ ep_status_t launch_on_device(const ep_buffer& b, LinearParams p, int64_t x_rows,
     const cuuint64_t dw[4] = {K, N, (cuuint64_t)p.parts, (cuuint64_t)weights},
                      sw[3] = {K * size, N * K * size, (cuuint64_t)p.wide * K * size};
     if (!encoder()) return fail(EP_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled");
-    if (!encode(&map_x, f8, p.x, 2, dx, sx, p.bn) || !encode(&map_w, f8, p.w, 4, dw, sw, 128))
+    if (!encode(&map_x, f8, p.x, 2, dx, sx, pair ? 128 : p.bn) || !encode(&map_w, f8, p.w, 4, dw, sw, 128))
         return fail(EP_ERR_UNSUPPORTED, "x or w is too large for a tensor map");
 
-    auto kernel = split ? (f8 ? linear_kernel<true, true> : linear_kernel<false, true>)
+    auto kernel = pair ? (f8 ? linear_pair_kernel<true> : linear_pair_kernel<false>) : split ? (f8 ? linear_kernel<true, true> : linear_kernel<false, true>)
                         : (f8 ? linear_kernel<true, false> : linear_kernel<false, false>);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
     if (e != cudaSuccess) return fail(EP_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-    const int64_t tiles = bound * p.nt;
+    const int64_t tiles = bound * p.nt, pairs = b.sm_count / 2;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(split ? tiles * p.splits : tiles < b.sm_count ? tiles : b.sm_count));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.gridDim = dim3((unsigned)(pair ? 2 * (tiles < pairs ? tiles : pairs) : split ? tiles * p.splits : tiles < b.sm_count ? tiles : b.sm_count));
+    cfg.blockDim = dim3(pair ? kPairThreads : kThreads);
+    cfg.dynamicSmemBytes = pair ? kPairSmem : smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = p.splits;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = pair ? 0 : 1;
     e = cudaLaunchKernelEx(&cfg, kernel, map_x, map_w, p);
     if (e != cudaSuccess) return fail(EP_ERR_CUDA, "linear launch: %s", cudaGetErrorString(e));
     set_last_error("");

@@ -106,6 +106,31 @@ def test_dense_depths(ep, kind, cin, rows):
     dense(ep, kind, rows, cin, 64, 3, False, True, "bf16")
 
 
+@pytest.mark.parametrize("act", [0, 1, 2, 3])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("out", ["bf16", "fp32", "e4m3"])
+@pytest.mark.parametrize("bias,res", [(False, False), (True, True)])
+def test_many_rows(ep, act, kind, out, bias, res):
+    """Rows enough for the widest tiles: whole and ragged ones, several to a CTA."""
+    for rows, cin, cout in ((256, 128, 256), (385, 384, 384), (1000, 256, 640)):
+        dense(ep, kind, rows, cin, cout, act, bias, res, out)
+
+
+@pytest.mark.parametrize("cout", [129, 250, 260, 264, 500, 516, 1000])
+@pytest.mark.parametrize("act", [0, 3])
+def test_many_rows_odd_widths(ep, cout, act):
+    for out in ("bf16", "fp32"):
+        dense(ep, "bf16", 300, 72, cout, act, True, True, out)
+    dense(ep, "e4m3", 270, 128, cout, act, True, True, "bf16")
+
+
+@pytest.mark.parametrize("kind,cin", [("bf16", 8), ("bf16", 1000), ("bf16", 7168), ("e4m3", 128), ("e4m3", 2048), ("e4m3", 7168)])
+def test_many_rows_depths(ep, kind, cin):
+    """More tiles than pairs of CTAs, so that the ring and the accumulators wrap from tile to tile."""
+    dense(ep, kind, 2600, cin, 2048, 0, False, False, "fp32")
+    dense(ep, kind, 2600, cin, 1024, 3, True, False, "bf16")
+
+
 @pytest.mark.parametrize("cout", [1, 2, 3, 5, 7, 9, 31, 63, 65, 127, 129, 191, 255, 257, 511, 1023])
 @pytest.mark.parametrize("act", [0, 3])
 def test_dense_odd_widths(ep, cout, act):
@@ -138,6 +163,8 @@ def routed(seed, n, e, k, mask=0.1, hot=0.0):
     (2, 300, 6, 2, 128, 136, 2, "bf16"),        # several tiles per expert
     (1, 700, 2, 1, 256, 384, 0, "e4m3"),
     (8, 16, 256, 8, 128, 128, 3, "bf16"),
+    (1, 4000, 5, 2, 128, 256, 3, "e4m3"),       # many rows per expert, unevenly
+    (2, 1500, 6, 3, 256, 300, 0, "bf16"),
     (1, 64, 1024, 4, 128, 64, 0, "fp32"),       # the most experts
 ])
 def test_experts(ep, kind, R, T, E, K, cin, cout, act, out):
