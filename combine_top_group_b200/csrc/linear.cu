@@ -682,7 +682,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         for (int id = first; ok && find_tile(p, cur, id, t); id += step) {
             const int ch = p.parts == 2 ? t.n * 128 : t.n * 256 + rank * 128, part = p.parts == 2 ? rank : 0;
             for (int k = 0; k < p.kblocks; ++k, ++i) {
-                if (wrap > 0) ok = __all_sync(FULL, tc::bar_wait_cluster(empty(s), (wrap - 1) & 1, stop));
+                if (wrap > 0) ok = __all_sync(FULL, tc::bar_wait(empty(s), (wrap - 1) & 1, stop));
                 if (!ok) break;
                 if (tc::elect()) {
                     const uint32_t at = ring + s * kPairStage, bar = tc::peer_smem(full(s), 0);
@@ -710,8 +710,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             for (int id = first; ok && find_tile(p, cur, id, t); id += step) {
                 for (int k = 0; k < p.kblocks; ++k) {
                     if ((F8 || k == 0) && acc >= 2)
-                        ok = __all_sync(FULL, tc::bar_wait_cluster(acc_empty(acc & 1), (acc / 2 - 1) & 1, stop));
-                    if (ok) ok = __all_sync(FULL, tc::bar_wait_cluster(full(s), wrap & 1, stop));
+                        ok = __all_sync(FULL, tc::bar_wait(acc_empty(acc & 1), (acc / 2 - 1) & 1, stop));
+                    if (ok) ok = __all_sync(FULL, tc::bar_wait(full(s), wrap & 1, stop));
                     if (!ok) break;
                     tc::fence_after();
                     const uint32_t at = ring + s * kPairStage;
@@ -764,38 +764,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 const float* xs = p.x_scale + (live ? row : t.row) * p.kblocks;
                 const float* w0 = p.w_scale + ((int64_t)g * p.parts * nb + (gated ? t.n : min(t.n * 2 + half, nb - 1))) * p.kblocks;
                 const float* w1 = gated ? w0 + (int64_t)nb * p.kblocks : w0;
-                float x_next = xs[0], w0_next = w0[0], w1_next = w1[0];
-                for (int k = 0; ok && k < p.kblocks; ++k, ++acc) {
-                    const float s0 = x_next * w0_next, s1 = x_next * w1_next;
-                    if (k + 1 < p.kblocks) {
-                        x_next = xs[k + 1];
-                        w0_next = w0[k + 1];
-                        w1_next = w1[k + 1];
+                // row scales four blocks at a time, and four ahead: a load that
+                // its own block waited for cost more than the block's products
+                float x4[4], x_next[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) x_next[q] = q < p.kblocks ? xs[q] : 0.f;
+#pragma unroll 1
+                for (int k0 = 0; ok && k0 < p.kblocks; k0 += 4) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        x4[q] = x_next[q];
+                        x_next[q] = k0 + 4 + q < p.kblocks ? xs[k0 + 4 + q] : 0.f;
                     }
-                    ok = __all_sync(FULL, tc::bar_wait_cluster(acc_full(acc & 1), (acc / 2) & 1, stop));
-                    if (!ok) break;
-                    tc::fence_after();
-                    if (rows > (warp & 3) * 32) {
-                        const uint32_t at = tmem + lane_base + (acc & 1) * 256;
-                        const uint64_t p0 = f32x2_pack(s0, s0), p1 = f32x2_pack(s1, s1);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t v[32];
-                            tc::tmem_ld32(at + column(c), v);
-                            tc::tmem_ld_wait();
+                    for (int q = 0; q < 4; ++q) {
+                        if (!ok || k0 + q >= p.kblocks) continue;
+                        const float s0 = x4[q] * w0[k0 + q], s1 = x4[q] * w1[k0 + q];
+                        ok = __all_sync(FULL, tc::bar_wait(acc_full(acc & 1), (acc / 2) & 1, stop));
+                        if (!ok) continue;
+                        tc::fence_after();
+                        if (rows > (warp & 3) * 32) {
+                            const uint32_t at = tmem + lane_base + (acc & 1) * 256;
+                            const uint64_t p0 = f32x2_pack(s0, s0), p1 = f32x2_pack(s1, s1);
 #pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                sum[c * 16 + j] =
-                                    f32x2_fma_rn(f32x2_pack(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])),
-                                                 c < 2 ? p0 : p1, sum[c * 16 + j]);
+                            for (int c = 0; c < 4; ++c) {
+                                uint32_t v[32];
+                                tc::tmem_ld32(at + column(c), v);
+                                tc::tmem_ld_wait();
+#pragma unroll
+                                for (int j = 0; j < 16; ++j)
+                                    sum[c * 16 + j] = f32x2_fma_rn(
+                                        f32x2_pack(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])),
+                                        c < 2 ? p0 : p1, sum[c * 16 + j]);
+                            }
                         }
+                        tc::fence_before();
+                        __syncwarp();
+                        if (lane == 0) tc::bar_arrive_at(empty_at[acc & 1]);
+                        ++acc;
                     }
-                    tc::fence_before();
-                    __syncwarp();
-                    if (lane == 0) tc::bar_arrive_at(empty_at[acc & 1]);
                 }
             } else {
-                ok = __all_sync(FULL, tc::bar_wait_cluster(acc_full(acc & 1), (acc / 2) & 1, stop));
+                ok = __all_sync(FULL, tc::bar_wait(acc_full(acc & 1), (acc / 2) & 1, stop));
                 tc::fence_after();
             }
             // all warps leave after the same tile: none may wait below for one that left

@@ -200,33 +200,11 @@ __device__ __forceinline__ void pair_commit(uint32_t bar) {
         "h"((uint16_t)3)
         : "memory");
 }
-// An arrival on a barrier of another CTA of the cluster.
+// An arrival on a barrier of another CTA of the cluster. It says that tensor
+// memory was read; no data in shared or global memory goes with it.
 __device__ __forceinline__ void bar_arrive_at(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-// bar_wait, with the acquire that arrivals from other CTAs need.
-__device__ __forceinline__ bool bar_try_cluster(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ bool bar_wait_cluster(uint32_t bar, uint32_t parity, volatile uint32_t* stop) {
-    if (bar_try_cluster(bar, parity)) return true;
-    const long long t0 = clock64();
-    while (!bar_try_cluster(bar, parity)) {
-        if (*stop) return false;
-        if (clock64() - t0 > kWaitLimitCycles) {
-            *stop = 1;
-            return false;
-        }
-    }
-    return true;
-}
-
 // ---- clusters ----------------------------------------------------------------
 
 __device__ __forceinline__ uint32_t cluster_rank() {
