@@ -17,6 +17,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "ep.h"
 #include "internal.h"
@@ -52,6 +54,7 @@ struct LinearParams {
     int stages;    // of the shared-memory ring
     int kblocks;   // 128-byte blocks of in_features
     int splits;    // CTAs of a cluster that share a tile's in_features
+    int acc_log;   // log2 of the accumulator sets
     uint32_t cols; // tensor-memory columns
     int vec;       // rows of out and residual allow 4-channel accesses
 };
@@ -85,8 +88,9 @@ constexpr int kMaxStages = 10;
 constexpr int kMaxBn = 128;
 // Shared memory: ring | staging (unsplit) | barriers and scales.
 constexpr int kStaging = 32 * 256 * 4;
-constexpr int kScales = 2 * 2 * kMaxBn * 4;
-constexpr int kControl = 256 + kScales;
+constexpr int kMaxAcc = 8;                      // accumulator sets in tensor memory
+constexpr int kScales = 1024 * 4;               // [sets][2][bn]
+constexpr int kControl = 512 + kScales;
 constexpr int kSmemMax = 227 * 1024;
 
 __host__ __device__ constexpr int stage_bytes(int na, int bn) { return na * kSub + bn * 128; }
@@ -255,16 +259,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* after = smem + (size_t)p.stages * sb;
     float* staging = reinterpret_cast<float*>(SPLIT ? smem : after);
     uint8_t* control = after + (SPLIT ? 0 : kStaging);
-    float* scales = reinterpret_cast<float*>(control + 256);  // [2][2][kMaxBn]
-    volatile uint32_t* stop = reinterpret_cast<uint32_t*>(control + 244);
+    float* scales = reinterpret_cast<float*>(control + 512);  // [sets][2][bn]
+    volatile uint32_t* stop = reinterpret_cast<uint32_t*>(control + 500);
     const uint32_t bars = tc::smem_u32(control);
     auto full = [&](int s) { return bars + 8 * s; };
     auto empty = [&](int s) { return bars + 8 * (kMaxStages + s); };
     auto acc_full = [&](int s) { return bars + 8 * (2 * kMaxStages + s); };
-    auto acc_empty = [&](int s) { return bars + 8 * (2 * kMaxStages + 2 + s); };
-    auto scale_full = [&](int s) { return bars + 8 * (2 * kMaxStages + 4 + s); };
-    const uint32_t drained = bars + 8 * (2 * kMaxStages + 6);
-    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(control + 240);
+    auto acc_empty = [&](int s) { return bars + 8 * (2 * kMaxStages + kMaxAcc + s); };
+    auto scale_full = [&](int s) { return bars + 8 * (2 * kMaxStages + 2 * kMaxAcc + s); };
+    const uint32_t drained = bars + 8 * (2 * kMaxStages + 3 * kMaxAcc);
+    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(control + 496);
+    const int sets = 1 << p.acc_log;
+    // set of the acc-th use, the parity of that use's phase, and of the one before it
+    auto set_of = [&](int acc) { return acc & (sets - 1); };
+    auto phase_of = [&](int acc) { return (uint32_t)(acc >> p.acc_log) & 1; };
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -272,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::bar_init(full(s), 1);
             tc::bar_init(empty(s), 1);
         }
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < sets; ++s) {
             tc::bar_init(acc_full(s), 1);
             tc::bar_init(acc_empty(s), kEpiWarps);
             tc::bar_init(scale_full(s), 32);
@@ -336,14 +344,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int subs = subs_of(p, t);
             const uint32_t idesc = tc::instr_desc(F8, 128, (t.rows + 15) / 16 * 16);
             for (int k = k_lo; k < k_hi; ++k) {
-                if ((F8 || k == k_lo) && acc >= 2)
-                    ok = __all_sync(FULL, tc::bar_wait(acc_empty(acc & 1), (acc / 2 - 1) & 1, stop));
+                if ((F8 || k == k_lo) && acc >= sets)
+                    ok = __all_sync(FULL, tc::bar_wait(acc_empty(set_of(acc)), phase_of(acc) ^ 1, stop));
                 if (ok) ok = __all_sync(FULL, tc::bar_wait(full(s), wrap & 1, stop));
                 if (!ok) break;
                 tc::fence_after();
                 const uint32_t at = ring + s * sb;
                 const uint64_t b = tc::smem_desc(at + p.na * kSub), w = tc::smem_desc(at);
-                const uint32_t d = tmem + (acc & 1) * p.na * p.bn;
+                const uint32_t d = tmem + set_of(acc) * p.na * p.bn;
                 const uint32_t keep = !F8 && k > k_lo ? 1u : 0u;
                 const bool last = F8 || k == k_hi - 1;
                 if (tc::elect()) {
@@ -356,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tc::mma<F8>(d + p.bn, w + kSub / 16 + 2 * q, b + 2 * q, idesc, q > 0 ? 1u : keep);
                     }
                     tc::commit(empty(s));
-                    if (last) tc::commit(acc_full(acc & 1));
+                    if (last) tc::commit(acc_full(set_of(acc)));
                 }
                 __syncwarp();
                 acc += last;
@@ -382,23 +390,48 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int a = 0; a < 2; ++a)
                     ws[a] = p.w_scale + ((int64_t)(t.group / p.R * p.parts + (p.parts == 2 ? a : 0)) * nb +
                                          min(channel_of(p, t, a) / 128, nb - 1)) * p.kblocks;
-                for (int k = k_lo; ok && k < k_hi; ++k, ++acc) {
-                    float xs[kMaxBn / 32];
+                // four blocks at a time, loaded four ahead: one load per block
+                // would hold each block up by its latency
+                float xn[kMaxBn / 32][4], wn[2][4];
+                auto fetch = [&](int k) {
 #pragma unroll
-                    for (int j = 0; j < kMaxBn / 32; ++j)
-                        xs[j] = lane + 32 * j < t.rows ? p.x_scale[(t.row + lane + 32 * j) * p.kblocks + k] : 0.f;
-                    const float w0 = ws[0][k], w1 = subs == 2 ? ws[1][k] : 0.f;
-                    if (acc >= 2) ok = tc::bar_wait(acc_empty(acc & 1), (acc / 2 - 1) & 1, stop);
-                    ok = __all_sync(FULL, ok);
-                    if (!ok) break;
-                    float* dst = scales + (acc & 1) * 2 * kMaxBn;
+                    for (int q = 0; q < 4; ++q) {
+                        const bool in = k + q < k_hi;
+                        wn[0][q] = in ? ws[0][k + q] : 0.f;
+                        wn[1][q] = in && subs == 2 ? ws[1][k + q] : 0.f;
 #pragma unroll
-                    for (int j = 0; j < kMaxBn / 32; ++j)
-                        if (32 * j < p.bn) {
-                            dst[lane + 32 * j] = xs[j] * w0;
-                            dst[kMaxBn + lane + 32 * j] = xs[j] * w1;
-                        }
-                    tc::bar_arrive(scale_full(acc & 1));
+                        for (int j = 0; j < kMaxBn / 32; ++j)
+                            xn[j][q] = in && lane + 32 * j < t.rows
+                                           ? p.x_scale[(t.row + lane + 32 * j) * p.kblocks + k + q] : 0.f;
+                    }
+                };
+                fetch(k_lo);
+#pragma unroll 1
+                for (int k = k_lo; ok && k < k_hi; k += 4) {
+                    float x4[kMaxBn / 32][4], w4[2][4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        w4[0][q] = wn[0][q];
+                        w4[1][q] = wn[1][q];
+#pragma unroll
+                        for (int j = 0; j < kMaxBn / 32; ++j) x4[j][q] = xn[j][q];
+                    }
+                    fetch(k + 4);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        if (!ok || k + q >= k_hi) continue;
+                        if (acc >= sets) ok = __all_sync(FULL, tc::bar_wait(acc_empty(set_of(acc)), phase_of(acc) ^ 1, stop));
+                        if (!ok) continue;
+                        float* dst = scales + set_of(acc) * 2 * p.bn;
+#pragma unroll
+                        for (int j = 0; j < kMaxBn / 32; ++j)
+                            if (32 * j < p.bn) {
+                                dst[lane + 32 * j] = x4[j][q] * w4[0][q];
+                                dst[p.bn + lane + 32 * j] = x4[j][q] * w4[1][q];
+                            }
+                        tc::bar_arrive(scale_full(set_of(acc)));
+                        ++acc;
+                    }
                 }
             }
         }
@@ -417,14 +450,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < kMaxBn / 2; ++i) sum[i] = 0;
                 for (int k = k_lo; ok && k < k_hi; ++k, ++acc) {
-                    ok = tc::bar_wait(acc_full(acc & 1), (acc / 2) & 1, stop) &&
-                         tc::bar_wait(scale_full(acc & 1), (acc / 2) & 1, stop);
+                    ok = tc::bar_wait(acc_full(set_of(acc)), phase_of(acc), stop) &&
+                         tc::bar_wait(scale_full(set_of(acc)), phase_of(acc), stop);
                     ok = __all_sync(FULL, ok);
                     if (!ok) break;
                     tc::fence_after();
                     if (sub < subs) {
-                        const ulonglong2* sc = reinterpret_cast<const ulonglong2*>(scales + ((acc & 1) * 2 + sub) * kMaxBn);
-                        const uint32_t at = tmem + lane_base + ((acc & 1) * p.na + sub) * p.bn;
+                        const ulonglong2* sc = reinterpret_cast<const ulonglong2*>(scales + (set_of(acc) * 2 + sub) * p.bn);
+                        const uint32_t at = tmem + lane_base + (set_of(acc) * p.na + sub) * p.bn;
 #pragma unroll
                         for (int c = 0; c < kMaxBn / 32; ++c) {
                             if (c * 32 >= t.rows) continue;
@@ -445,15 +478,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     tc::fence_before();
                     __syncwarp();
-                    if (lane == 0) tc::bar_arrive(acc_empty(acc & 1));
+                    if (lane == 0) tc::bar_arrive(acc_empty(set_of(acc)));
                 }
             } else {
-                ok = __all_sync(FULL, tc::bar_wait(acc_full(acc & 1), (acc / 2) & 1, stop));
+                ok = __all_sync(FULL, tc::bar_wait(acc_full(set_of(acc)), phase_of(acc), stop));
                 tc::fence_after();
             }
             // all warps leave after the same tile: none may wait below for one that left
             ok = epi_sync_and(ok);
-            const uint32_t at = tmem + lane_base + ((acc & 1) * p.na + sub) * p.bn;
+            const uint32_t at = tmem + lane_base + (set_of(acc) * p.na + sub) * p.bn;
             const int width = subs * 128;
 #pragma unroll
             for (int c = 0; c < kMaxBn / 32; ++c) {
@@ -488,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!F8) {
                 tc::fence_before();
                 __syncwarp();
-                if (lane == 0) tc::bar_arrive(acc_empty(acc & 1));
+                if (lane == 0) tc::bar_arrive(acc_empty(set_of(acc)));
                 ++acc;
             }
         }
@@ -951,8 +984,80 @@ LinearParams params_of(const ep_linear_t& q) {
     return p;
 }
 
-// Pairs of CTAs take 256 rows at a time.
-bool use_pair(const LinearParams& p, int64_t avg) { return avg >= 256 && p.wide >= 256; }
+constexpr int kMaxSplits = 8;
+
+// Clusters of n CTAs, one CTA per SM, that device b can hold at once: fewer
+// than SMs / n, since a cluster stays within a GPC (15 of 8, not 18).
+int clusters_of(const ep_buffer& b, int n) {
+    static std::atomic<int> known[64][kMaxSplits + 1];
+    std::atomic<int>* at = b.device >= 0 && b.device < 64 ? &known[b.device][n] : nullptr;
+    int count = at ? at->load(std::memory_order_relaxed) : 0;
+    if (count > 0) return count - 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(n * b.sm_count));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemMax;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = n;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const auto kernel = linear_kernel<false, true>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&count, kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        count = 0;
+    }
+    if (at) at->store(count + 1, std::memory_order_relaxed);
+    return count;
+}
+
+// How a call is tiled.
+struct Shape {
+    bool pair;
+    int bn, na, nt, splits;
+    int64_t bound;  // row tiles there can be
+};
+
+// Takes the kernel with the least time by this estimate, in microseconds for
+// 128 bytes of in_features: 0.28 (bf16) or 0.88 (e4m3) for a pair's 256 x 256
+// tile; 0.50 or 1.34 for a CTA's 128 rows x 256 channels, 0.28 where its rows
+// are few (it then waits for weights alone). An expert's last tile is half
+// empty in the mean: of 256 rows with pairs, of 16 columns without.
+Shape shape_of(const ep_buffer& b, const LinearParams& p, int64_t avg, int64_t most) {
+    const bool f8 = p.x_scale != nullptr;
+    const int64_t groups = most < p.G ? most : p.G;
+    auto tiles = [&](int rows) { return p.G == 1 ? (avg + rows - 1) / rows : groups * ((avg + rows - 1) / rows); };
+    Shape c{};
+    c.bn = avg <= 32 ? 32 : avg <= 64 ? 64 : 128;
+    c.bound = p.cnt ? (int64_t)p.G * ((p.region + c.bn - 1) / c.bn) : most / c.bn + groups;
+    const int64_t likely = tiles(c.bn);
+    // two weight tiles per CTA share its rows of x; one where tiles are few
+    c.na = 2;
+    c.nt = p.parts == 2 ? (p.N + 127) / 128 : (p.N + 255) / 256;
+    if (p.parts == 1 && (p.N <= 128 || likely * c.nt < b.sm_count)) {
+        c.na = 1;
+        c.nt = (p.N + 127) / 128;
+    }
+    // few tiles: a cluster shares each, as many CTAs as the device can hold clusters of
+    c.splits = 1;
+    for (int n = 2; n <= kMaxSplits; ++n)
+        if (likely * c.nt <= clusters_of(b, n) && p.kblocks >= 4 * n && c.bound * c.nt * n <= 4 * b.sm_count) c.splits = n;
+    if (avg < 256 || p.wide < 256) return c;
+    const double rounds_c = (double)likely * c.nt / b.sm_count, rounds_p =
+        (p.G == 1 ? (double)tiles(256) : groups * (avg / 256.0 + 0.5)) * ((p.wide + 255) / 256) / (b.sm_count / 2);
+    const double time_c = (rounds_c < 1 ? 1.0 / c.splits : rounds_c) * (f8 ? 1.34 : 0.50) * c.na / 2;
+    const double time_p = (rounds_p < 1 ? 1.0 : rounds_p) * (f8 ? 0.88 : 0.28);
+    if (time_p > time_c) return c;
+    c.pair = true;
+    c.bn = 256;
+    c.na = 2;
+    c.splits = 1;
+    c.nt = p.parts == 2 ? (p.N + 127) / 128 : (p.N + 255) / 256;
+    c.bound = p.cnt ? (int64_t)p.G * ((p.region + 255) / 256) : most / 256 + groups;
+    return c;
+}
 
 // Chooses tile, split and grid and launches. x_rows: rows that x holds;
 // weights: matrices in w; avg: rows of a group to expect (any count is right).
@@ -961,25 +1066,15 @@ ep_status_t launch_on_device(const ep_buffer& b, LinearParams p, int64_t x_rows,
     const bool f8 = p.x_scale != nullptr;
     const int size = f8 ? 1 : 2;
     p.kblocks = f8 ? p.K / 128 : (p.K + 63) / 64;
-    const bool pair = use_pair(p, avg);
-    p.bn = pair ? 256 : avg <= 32 ? 32 : avg <= 64 ? 64 : 128;
     p.vec = p.N % 4 == 0;
-    // row tiles there can be, and that are likely
-    const int64_t groups = most < p.G ? most : p.G;
-    const int64_t bound = (p.cnt ? (int64_t)p.G * ((p.region + p.bn - 1) / p.bn) : most / p.bn + groups);
-    const int64_t likely = groups * ((avg + p.bn - 1) / p.bn);
-    // two weight tiles per CTA share its rows of x; one where tiles are few
-    p.na = 2;
-    p.nt = p.parts == 2 ? (p.N + 127) / 128 : (p.N + 255) / 256;
-    if (!pair && p.parts == 1 && (p.N <= 128 || likely * p.nt < b.sm_count)) {
-        p.na = 1;
-        p.nt = (p.N + 127) / 128;
-    }
+    const Shape c = shape_of(b, p, avg, most);
+    const bool pair = c.pair;
+    p.bn = c.bn;
+    p.na = c.na;
+    p.nt = c.nt;
+    p.splits = c.splits;
+    const int64_t bound = c.bound;
     if (bound * p.nt >= (int64_t)1 << 30) return fail(EP_ERR_UNSUPPORTED, "too many tiles: rows x out_features");
-    p.splits = 1;
-    while (!pair && p.splits < 8 && 2 * p.splits * likely * p.nt <= b.sm_count && p.kblocks >= 4 * p.splits &&
-           bound * p.nt * 2 * p.splits <= 4 * b.sm_count)
-        p.splits *= 2;
     const bool split = p.splits > 1;
     const int sb = stage_bytes(p.na, p.bn);
     const int fixed = kControl + (split ? 0 : kStaging) + 1024;  // 1024: alignment of the ring
@@ -987,8 +1082,11 @@ ep_status_t launch_on_device(const ep_buffer& b, LinearParams p, int64_t x_rows,
     if (p.stages > kMaxStages) p.stages = kMaxStages;
     // a split CTA stages its whole tile in the ring
     const int smem = p.stages * sb + fixed;
-    p.cols = 32;
-    while ((int)p.cols < 2 * p.na * p.bn) p.cols *= 2;
+    // bf16 fills one set while another is read; e4m3 hands a set over for each
+    // block, and more of them hide the hand-over
+    const int sets = f8 && p.na * p.bn <= 128 ? (p.na * p.bn <= 64 ? 8 : 4) : 2;
+    p.acc_log = sets == 8 ? 3 : sets == 4 ? 2 : 1;
+    p.cols = sets * p.na * p.bn;
 
     CUtensorMap map_x, map_w;
     const cuuint64_t K = p.K, N = p.N;
