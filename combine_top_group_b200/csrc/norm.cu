@@ -154,6 +154,209 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(NormParams p) {
     }
 }
 
+// ---- streams of rows -----------------------------------------------------------
+// A call with rows for every CTA several times over runs persistent CTAs. Each
+// group of up to 32 lanes loads its own part of the next rows into shared
+// memory with cp.async while it works on one: loads stay in flight across the
+// reduction and the stores, no warp reads what another loaded, and gamma and
+// the dgamma sums stay in registers. A thread holds 16 neighbouring channels
+// (8 lanes to a scale block); the arithmetic runs on pairs of fp32 values,
+// since the instruction rate bounds the e4m3 cast and the gradient otherwise
+// (77% of issue slots with scalar arithmetic on 8 channels per thread).
+
+__device__ __forceinline__ uint32_t smem_of(const void* p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most N of the thread's groups are in flight.
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint64_t f32x2_add_rn(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t widen(uint32_t u) { return f32x2_pack(bf16lo(u), bf16hi(u)); }
+__device__ __forceinline__ uint32_t narrow(uint64_t v) {
+    const float2 f = f32x2_unpack(v);
+    return pack_bf16x2(f.x, f.y);
+}
+// 16 channels of bf16 as 8 fp32 pairs, and back.
+__device__ __forceinline__ void widen16(const uint4 (&a)[2], uint64_t (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        v[4 * i] = widen(a[i].x);
+        v[4 * i + 1] = widen(a[i].y);
+        v[4 * i + 2] = widen(a[i].z);
+        v[4 * i + 3] = widen(a[i].w);
+    }
+}
+__device__ __forceinline__ void store16(uint16_t* p, const uint64_t (&v)[8]) {
+    u32x8 o;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o.v[i] = narrow(v[i]);
+    st256(p, o);
+}
+
+// Rows of a slot in shared memory: as many as leave room for VPT vectors of
+// each array for 512 threads.
+__host__ __device__ constexpr int depth_of(int vpt, int arrays) { return vpt == 1 ? 4 : arrays < 3 ? 3 : 2; }
+
+// Where a thread stands: its row of the CTA's, its place in it, and its group
+// of lanes, which loads for itself.
+struct Place {
+    int rpc, sub, t;
+    int group, lane, first;  // group size; the thread's lane and the group's first 16-byte chunk of the row
+};
+__device__ __forceinline__ Place place_of(int tpr) {
+    Place q;
+    q.rpc = blockDim.x / tpr;
+    q.sub = threadIdx.x / tpr;
+    q.t = threadIdx.x - q.sub * tpr;
+    q.group = tpr < 32 ? tpr : 32;
+    q.lane = q.t & (q.group - 1);
+    q.first = (q.t - q.lane) * 2;
+    return q;
+}
+// The chunks of vector j, array a, ring position `stage`: 2 per thread.
+template <int VPT, int A>
+__device__ __forceinline__ uint4* chunks_of(uint4* ring, const Place& q, int tpr, int stage, int a, int j) {
+    return ring + (((stage * A + a) * VPT + j) * q.rpc + q.sub) * (tpr * 2) + q.first;
+}
+template <int VPT, int A>
+__device__ __forceinline__ void load_ahead(uint4* ring, const Place& q, int tpr, int nv, int stage, int a,
+                                           const uint16_t* row) {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        uint4* dst = chunks_of<VPT, A>(ring, q, tpr, stage, a, j);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int c = h * q.group + q.lane, at = j * tpr * 2 + q.first + c;
+            if (at < nv * 2) cp_async16(smem_of(dst + c), row + at * 8);
+        }
+    }
+}
+// The thread's 16 channels. Lanes 4-7 of each 8 take their second half first:
+// otherwise lanes 4 apart would meet in the same banks.
+template <int VPT, int A>
+__device__ __forceinline__ void read16(uint4* ring, const Place& q, int tpr, int stage, int a, int j, uint64_t (&v)[8]) {
+    const uint4* src = chunks_of<VPT, A>(ring, q, tpr, stage, a, j) + 2 * q.lane;
+    const int h = (q.lane >> 2) & 1;
+    const uint4 x = src[h], y = src[h ^ 1];
+    const uint4 b[2] = {h ? y : x, h ? x : y};
+    widen16(b, v);
+}
+
+__device__ __forceinline__ void load_gamma_pairs(const void* gamma, int fp32, int c, uint64_t (&g)[8]) {
+    float f[kVec];
+    load_gamma(gamma, fp32, c, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = f32x2_pack(f[2 * i], f[2 * i + 1]);
+}
+
+// Sum over the row's threads: shuffles within a group, shared memory beyond.
+__device__ __forceinline__ float stream_sum(uint64_t pairs, int tpr, float* red) {
+    const float2 f = f32x2_unpack(pairs);
+    float v = f.x + f.y;
+    if (tpr >= 32) return row_sum(v, tpr, red);
+    for (int o = tpr >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
+    return v;
+}
+
+template <int VPT, bool RES>
+__global__ void __launch_bounds__(512) rmsnorm_stream_kernel(NormParams p) {
+    extern __shared__ __align__(16) uint4 ring[];
+    __shared__ float red[2][32];
+    constexpr int A = RES ? 2 : 1, kDepth = depth_of(VPT, A);
+    const Place q = place_of(p.tpr);
+    const int64_t step = (int64_t)gridDim.x * q.rpc, row_first = (int64_t)blockIdx.x * q.rpc;
+    auto issue = [&](int64_t row0, int stage) {
+        const int64_t row = row0 + q.sub;
+        if (row < p.N) {
+            load_ahead<VPT, A>(ring, q, p.tpr, p.nv, stage, 0, p.x + row * p.H);
+            if (RES) load_ahead<VPT, A>(ring, q, p.tpr, p.nv, stage, A - 1, p.res + row * p.H);
+        }
+        cp_commit();
+    };
+    uint64_t g[VPT][8];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+        if (q.t + j * p.tpr < p.nv) load_gamma_pairs(p.gamma, p.gamma_fp32, (q.t + j * p.tpr) * kVec, g[j]);
+#pragma unroll
+    for (int s = 0; s < kDepth - 1; ++s) issue(row_first + s * step, s);
+    int stage = 0, flip = 0;
+    for (int64_t row0 = row_first; row0 < p.N; row0 += step, flip ^= 1) {
+        __syncwarp();  // the slot filled next was read by the whole group
+        issue(row0 + (kDepth - 1) * step, stage == 0 ? kDepth - 1 : stage - 1);
+        cp_wait<kDepth - 1>();
+        __syncwarp();  // every lane's copies of this row are done
+        const int64_t row = row0 + q.sub;
+        const bool live = row < p.N;
+        uint64_t v[VPT][8], ss = 0;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[j][i] = 0;
+            if (live && q.t + j * p.tpr < p.nv) {
+                read16<VPT, A>(ring, q, p.tpr, stage, 0, j, v[j]);
+                if (RES) {
+                    uint64_t r[8];
+                    read16<VPT, A>(ring, q, p.tpr, stage, A - 1, j, r);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[j][i] = f32x2_add_rn(v[j][i], r[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) ss = f32x2_fma_rn(v[j][i], v[j][i], ss);
+            }
+        }
+        const float rstd = 1.0f / sqrtf(stream_sum(ss, p.tpr, red[flip]) * p.inv_h + p.eps);
+        if (live && q.t == 0 && p.rstd) p.rstd[row] = rstd;
+        const uint64_t rr = f32x2_pack(rstd, rstd);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int k = q.t + j * p.tpr;
+            const bool on = live && k < p.nv;
+            const int64_t at = row * p.H + k * kVec;
+            if (on && p.h) store16(p.h + at, v[j]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[j][i] = f32x2_mul_rn(f32x2_mul_rn(v[j][i], rr), g[j][i]);
+            if (on && p.y) store16(p.y + at, v[j]);
+            if (p.q) {
+                float amax = 1e-4f;
+                if (on) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 f = f32x2_unpack(v[j][i]);
+                        amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    }
+                }
+#pragma unroll
+                for (int off = 1; off < 8; off <<= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, off));
+                if (on) {
+                    const float s = 448.0f / amax;
+                    const uint64_t s2 = f32x2_pack(s, s);
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 a = f32x2_unpack(f32x2_mul_rn(v[j][2 * i], s2)),
+                                     b = f32x2_unpack(f32x2_mul_rn(v[j][2 * i + 1], s2));
+                        w[i] = pack_e4m3x2(a.x, a.y) | pack_e4m3x2(b.x, b.y) << 16;
+                    }
+                    *reinterpret_cast<uint4*>(p.q + at) = make_uint4(w[0], w[1], w[2], w[3]);
+                    if ((k & 7) == 0) p.q_scale[row * (p.H / 128) + k / 8] = amax / 448.0f;
+                }
+            }
+        }
+        stage = stage == kDepth - 1 ? 0 : stage + 1;
+    }
+}
+
 struct NormBwdParams {
     int64_t N;
     int H, nv, tpr;
@@ -244,19 +447,119 @@ __global__ void __launch_bounds__(1024) rmsnorm_bwd_kernel(NormBwdParams p) {
     }
 }
 
-// dgamma[c] = sum of the slots' partial rows, in slot order within each of 8
+// rmsnorm_bwd_kernel on a stream of rows. At the end a CTA adds its rows-per-CTA
+// dgamma sums through shared memory, in row order, and writes one partial row.
+template <int VPT, bool DH>
+__global__ void __launch_bounds__(512) rmsnorm_bwd_stream_kernel(NormBwdParams p) {
+    extern __shared__ __align__(16) uint4 ring[];
+    __shared__ float red[2][32];
+    constexpr int A = DH ? 3 : 2, kDepth = depth_of(VPT, A);
+    const Place q = place_of(p.tpr);
+    const int64_t step = (int64_t)gridDim.x * q.rpc, row_first = (int64_t)blockIdx.x * q.rpc;
+    auto issue = [&](int64_t row0, int stage) {
+        const int64_t row = row0 + q.sub;
+        if (row < p.N) {
+            load_ahead<VPT, A>(ring, q, p.tpr, p.nv, stage, 0, p.h + row * p.H);
+            load_ahead<VPT, A>(ring, q, p.tpr, p.nv, stage, 1, p.dy + row * p.H);
+            if (DH) load_ahead<VPT, A>(ring, q, p.tpr, p.nv, stage, A - 1, p.dh + row * p.H);
+        }
+        cp_commit();
+    };
+    uint64_t g[VPT][8], dg[VPT][8];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        if (q.t + j * p.tpr < p.nv) load_gamma_pairs(p.gamma, p.gamma_fp32, (q.t + j * p.tpr) * kVec, g[j]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dg[j][i] = 0;
+    }
+#pragma unroll
+    for (int s = 0; s < kDepth - 1; ++s) issue(row_first + s * step, s);
+    int stage = 0, flip = 0;
+    float rstd_next = row_first + q.sub < p.N ? p.rstd[row_first + q.sub] : 0.f;
+    for (int64_t row0 = row_first; row0 < p.N; row0 += step, flip ^= 1) {
+        __syncwarp();  // the slot filled next was read by the whole group
+        issue(row0 + (kDepth - 1) * step, stage == 0 ? kDepth - 1 : stage - 1);
+        const int64_t row = row0 + q.sub;
+        const bool live = row < p.N;
+        const float rstd = rstd_next;
+        if (row + step < p.N) rstd_next = p.rstd[row + step];
+        cp_wait<kDepth - 1>();
+        __syncwarp();  // every lane's copies of this row are done
+        const uint64_t rr = f32x2_pack(rstd, rstd);
+        uint64_t n[VPT][8], dt[VPT][8], dot = 0;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            if (live && q.t + j * p.tpr < p.nv) {
+                read16<VPT, A>(ring, q, p.tpr, stage, 0, j, n[j]);
+                read16<VPT, A>(ring, q, p.tpr, stage, 1, j, dt[j]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    n[j][i] = f32x2_mul_rn(n[j][i], rr);
+                    dg[j][i] = f32x2_fma_rn(dt[j][i], n[j][i], dg[j][i]);
+                    dt[j][i] = f32x2_mul_rn(dt[j][i], g[j][i]);
+                    dot = f32x2_fma_rn(dt[j][i], n[j][i], dot);
+                }
+            }
+        }
+        const float m = -stream_sum(dot, p.tpr, red[flip]) * p.inv_h;
+        const uint64_t mm = f32x2_pack(m, m);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int k = q.t + j * p.tpr;
+            if (live && k < p.nv) {
+                uint64_t o[8];
+                if (DH) {
+                    read16<VPT, A>(ring, q, p.tpr, stage, A - 1, j, o);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) o[i] = 0;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] = f32x2_fma_rn(f32x2_fma_rn(n[j][i], mm, dt[j][i]), rr, o[i]);
+                store16(p.dx + row * p.H + k * kVec, o);
+            }
+        }
+        stage = stage == kDepth - 1 ? 0 : stage + 1;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    float* sums = reinterpret_cast<float*>(ring);  // [rpc][H]
+    float* out = p.part + (int64_t)blockIdx.x * p.H;
+    if (q.rpc > 1) __syncthreads();  // every thread is done with its slots
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int k = q.t + j * p.tpr;
+        if (k < p.nv) {
+            float4* o = reinterpret_cast<float4*>((q.rpc > 1 ? sums + (int64_t)q.sub * p.H : out) + k * kVec);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 a = f32x2_unpack(dg[j][2 * i]), b = f32x2_unpack(dg[j][2 * i + 1]);
+                o[i] = make_float4(a.x, a.y, b.x, b.y);
+            }
+        }
+    }
+    if (q.rpc > 1) {
+        __syncthreads();
+        for (int c = threadIdx.x; c < p.H; c += blockDim.x) {
+            float a = sums[c];
+            for (int i = 1; i < q.rpc; ++i) a += sums[i * p.H + c];
+            out[c] = a;
+        }
+    }
+}
+
+// dgamma[c] = sum of the partial rows, in slot order within each of 32
 // strides, then over the strides.
-__global__ void __launch_bounds__(256) dgamma_kernel(const float* part, int slots, int H, float* dgamma) {
-    __shared__ float s[8][33];
+__global__ void __launch_bounds__(1024) dgamma_kernel(const float* part, int slots, int H, float* dgamma) {
+    __shared__ float s[32][33];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     float a = 0.f;
-    for (int i = w; i < slots; i += 8) a += part[(int64_t)i * H + c];
+    for (int i = w; i < slots; i += 32) a += part[(int64_t)i * H + c];
     s[w][lane] = a;
     __syncthreads();
     if (w == 0) {
 #pragma unroll
-        for (int i = 1; i < 8; ++i) a += s[i][lane];
+        for (int i = 1; i < 32; ++i) a += s[i][lane];
         dgamma[c] = a;
     }
 }
@@ -271,14 +574,41 @@ void shape_of(int H, int* nv, int* tpr, int* vpt) {
 
 int rows_per_cta(int tpr) { return tpr >= 256 ? 1 : 256 / tpr; }
 
+// The stream kernels: a power of two of lanes up to a warp, or whole warps.
+bool stream_shape(int H, int* nv, int* tpr, int* vpt) {
+    if (H > 16384) return false;
+    *nv = H / kVec;
+    *vpt = *nv <= 512 ? 1 : 2;
+    const int n = (*nv + *vpt - 1) / *vpt;
+    *tpr = n <= 8 ? 8 : n <= 16 ? 16 : (n + 31) / 32 * 32;
+    return true;
+}
+int stream_rows(int tpr) { return 512 / tpr; }
+
 // Partial dgamma rows of a backward call, at most.
-constexpr int64_t kMaxSlots = 1184;
+constexpr int64_t kMaxSlots = 592;
+
+// A stream kernel runs from this many row groups on.
+constexpr int64_t kStreamRows = 592;
 
 int64_t bwd_slots(int64_t N, int tpr) {
     const int rpc = rows_per_cta(tpr);
     const int64_t rows = (N + rpc - 1) / rpc * rpc;
     const int64_t most = kMaxSlots / rpc * rpc;
     return rows < most ? rows : most;
+}
+
+// CTAs that the device holds at once; 0 on an error.
+int resident(const void* kernel, int threads, int smem) {
+    int dev = 0, sms = 0, per = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, smem) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return per * sms;
 }
 
 ep_status_t check_shape(int64_t N, int H, int gamma_type) {
@@ -338,9 +668,25 @@ ep_status_t ep_rmsnorm(int64_t N, int H, const void* d_x, const void* d_residual
     p.q = static_cast<uint8_t*>(d_q);
     p.q_scale = d_q_scale;
     p.rstd = d_rstd;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    NormParams ps = p;
+    int svpt;
+    if (stream_shape(H, &ps.nv, &ps.tpr, &svpt)) {
+        const int rps = stream_rows(ps.tpr), threads = rps * ps.tpr;
+        const int arrays = ps.res ? 2 : 1, smem = depth_of(svpt, arrays) * arrays * svpt * threads * 32;
+        const auto kernel = svpt == 1 ? (ps.res ? rmsnorm_stream_kernel<1, true> : rmsnorm_stream_kernel<1, false>)
+                                      : (ps.res ? rmsnorm_stream_kernel<2, true> : rmsnorm_stream_kernel<2, false>);
+        const int64_t groups = (N + rps - 1) / rps;
+        if (groups >= kStreamRows) {
+            const int ctas = resident((const void*)kernel, threads, smem);
+            if (ctas > 0) {
+                kernel<<<(unsigned)(groups < ctas ? groups : ctas), threads, smem, s>>>(ps);
+                return launched("rmsnorm");
+            }
+        }
+    }
     const int rpc = rows_per_cta(p.tpr);
     const unsigned grid = (unsigned)((N + rpc - 1) / rpc);
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (vpt == 1) rmsnorm_kernel<1><<<grid, p.tpr * rpc, 0, s>>>(p);
     else if (vpt == 2) rmsnorm_kernel<2><<<grid, p.tpr * rpc, 0, s>>>(p);
     else rmsnorm_kernel<4><<<grid, p.tpr * rpc, 0, s>>>(p);
@@ -398,13 +744,32 @@ ep_status_t ep_rmsnorm_backward(int64_t N, int H, const void* d_h, const float* 
     p.dh = static_cast<const uint16_t*>(d_dh);
     p.dx = static_cast<uint16_t*>(d_dx);
     p.part = static_cast<float*>(d_workspace);
+    NormBwdParams ps = p;
+    int svpt;
+    if (stream_shape(H, &ps.nv, &ps.tpr, &svpt)) {
+        const int rps = stream_rows(ps.tpr), threads = rps * ps.tpr;
+        const int arrays = ps.dh ? 3 : 2, smem = depth_of(svpt, arrays) * arrays * svpt * threads * 32;
+        const auto kernel =
+            svpt == 1 ? (ps.dh ? rmsnorm_bwd_stream_kernel<1, true> : rmsnorm_bwd_stream_kernel<1, false>)
+                      : (ps.dh ? rmsnorm_bwd_stream_kernel<2, true> : rmsnorm_bwd_stream_kernel<2, false>);
+        const int64_t groups = (N + rps - 1) / rps;
+        int64_t ctas = resident((const void*)kernel, threads, smem);
+        if (ctas > kMaxSlots) ctas = kMaxSlots;
+        if (groups < ctas) ctas = groups;
+        if (ctas > 0) {
+            kernel<<<(unsigned)ctas, threads, smem, s>>>(ps);
+            if (ep_status_t st = launched("rmsnorm backward")) return st;
+            dgamma_kernel<<<H / 32, 1024, 0, s>>>(p.part, (int)ctas, H, d_dgamma);
+            return launched("dgamma");
+        }
+    }
     const int rpc = rows_per_cta(p.tpr);
     const int slots = (int)bwd_slots(N, p.tpr);
     if (vpt == 1) rmsnorm_bwd_kernel<1><<<slots / rpc, p.tpr * rpc, 0, s>>>(p);
     else if (vpt == 2) rmsnorm_bwd_kernel<2><<<slots / rpc, p.tpr * rpc, 0, s>>>(p);
     else rmsnorm_bwd_kernel<4><<<slots / rpc, p.tpr * rpc, 0, s>>>(p);
     if (ep_status_t st = launched("rmsnorm backward")) return st;
-    dgamma_kernel<<<H / 32, 256, 0, s>>>(p.part, slots, H, d_dgamma);
+    dgamma_kernel<<<H / 32, 1024, 0, s>>>(p.part, slots, H, d_dgamma);
     return launched("dgamma");
 }
 
