@@ -68,12 +68,13 @@ __device__ __forceinline__ float row_sum(float v, int tpr, float* red) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
     if (tpr == 32) return v;
-    const int warp = threadIdx.x >> 5, wpr = tpr >> 5, first = warp / wpr * wpr;
+    const int warp = threadIdx.x >> 5, wpr = tpr >> 5, first = (int)threadIdx.x / tpr * wpr;
     if ((threadIdx.x & 31) == 0) red[warp] = v;
     __syncthreads();
-    float s = 0.f;
-    for (int w = 0; w < wpr; ++w) s += red[first + w];
-    return s;
+    v = (int)(threadIdx.x & 31) < wpr ? red[first + (threadIdx.x & 31)] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
+    return v;
 }
 
 template <int VPT>
@@ -111,7 +112,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(NormParams p) {
         }
     }
     ss = row_sum(ss, p.tpr, red);
-    const float rstd = 1.0f / sqrtf(ss * p.inv_h + p.eps);
+    const float rstd = rsqrtf(ss * p.inv_h + p.eps);
     if (live && t == 0 && p.rstd) p.rstd[row] = rstd;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
@@ -208,48 +209,48 @@ __device__ __forceinline__ void store16(uint16_t* p, const uint64_t (&v)[8]) {
 // each array for 512 threads.
 __host__ __device__ constexpr int depth_of(int vpt, int arrays) { return vpt == 1 ? 4 : arrays < 3 ? 3 : 2; }
 
-// Where a thread stands: its row of the CTA's, its place in it, and its group
-// of lanes, which loads for itself.
+// Where a thread stands: its row of the CTA's and its place in it; what it
+// loads (chunks of 16 bytes: its lane's, and one group further) and reads (two
+// neighbouring chunks) of a vector, as byte offsets.
 struct Place {
     int rpc, sub, t;
-    int group, lane, first;  // group size; the thread's lane and the group's first 16-byte chunk of the row
+    uint32_t load, load_step, read;
+    uint32_t plane;   // bytes from one vector, array or ring position to the next
+    int from, next;   // first channels of the two chunks it loads, within its vector
 };
 __device__ __forceinline__ Place place_of(int tpr) {
     Place q;
     q.rpc = blockDim.x / tpr;
     q.sub = threadIdx.x / tpr;
     q.t = threadIdx.x - q.sub * tpr;
-    q.group = tpr < 32 ? tpr : 32;
-    q.lane = q.t & (q.group - 1);
-    q.first = (q.t - q.lane) * 2;
+    const int group = tpr < 32 ? tpr : 32, lane = q.t & (group - 1), first = (q.t - lane) * 2;
+    const uint32_t row = q.sub * tpr * 2;
+    q.load = (row + first + lane) * 16;
+    q.load_step = group * 16;
+    // Lanes 4-7 of each 8 take their second half first: otherwise lanes 4
+    // apart would meet in the same banks.
+    q.read = (row + 2 * q.t + ((lane >> 2) & 1)) * 16;
+    q.plane = blockDim.x * 32;
+    q.from = (first + lane) * 8;
+    q.next = q.from + group * 8;
     return q;
 }
-// The chunks of vector j, array a, ring position `stage`: 2 per thread.
-template <int VPT, int A>
-__device__ __forceinline__ uint4* chunks_of(uint4* ring, const Place& q, int tpr, int stage, int a, int j) {
-    return ring + (((stage * A + a) * VPT + j) * q.rpc + q.sub) * (tpr * 2) + q.first;
-}
-template <int VPT, int A>
-__device__ __forceinline__ void load_ahead(uint4* ring, const Place& q, int tpr, int nv, int stage, int a,
-                                           const uint16_t* row) {
+// Loads the thread's chunks of a row into the planes from dst on.
+template <int VPT>
+__device__ __forceinline__ void load_ahead(uint32_t dst, const Place& q, int tpr, int H, const uint16_t* row) {
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-        uint4* dst = chunks_of<VPT, A>(ring, q, tpr, stage, a, j);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int c = h * q.group + q.lane, at = j * tpr * 2 + q.first + c;
-            if (at < nv * 2) cp_async16(smem_of(dst + c), row + at * 8);
-        }
+        const int at = j * tpr * kVec;
+        if (at + q.from < H) cp_async16(dst + j * q.plane + q.load, row + at + q.from);
+        if (at + q.next < H) cp_async16(dst + j * q.plane + q.load + q.load_step, row + at + q.next);
     }
 }
-// The thread's 16 channels. Lanes 4-7 of each 8 take their second half first:
-// otherwise lanes 4 apart would meet in the same banks.
-template <int VPT, int A>
-__device__ __forceinline__ void read16(uint4* ring, const Place& q, int tpr, int stage, int a, int j, uint64_t (&v)[8]) {
-    const uint4* src = chunks_of<VPT, A>(ring, q, tpr, stage, a, j) + 2 * q.lane;
-    const int h = (q.lane >> 2) & 1;
-    const uint4 x = src[h], y = src[h ^ 1];
-    const uint4 b[2] = {h ? y : x, h ? x : y};
+// The thread's 16 channels of a plane.
+__device__ __forceinline__ void read16(const uint8_t* plane, const Place& q, uint64_t (&v)[8]) {
+    const bool second = q.read & 16;
+    const uint4 x = *reinterpret_cast<const uint4*>(plane + q.read),
+                y = *reinterpret_cast<const uint4*>(plane + (q.read ^ 16));
+    const uint4 b[2] = {second ? y : x, second ? x : y};
     widen16(b, v);
 }
 
@@ -271,29 +272,37 @@ __device__ __forceinline__ float stream_sum(uint64_t pairs, int tpr, float* red)
 
 template <int VPT, bool RES>
 __global__ void __launch_bounds__(512) rmsnorm_stream_kernel(NormParams p) {
-    extern __shared__ __align__(16) uint4 ring[];
+    extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float red[2][32];
     constexpr int A = RES ? 2 : 1, kDepth = depth_of(VPT, A);
     const Place q = place_of(p.tpr);
     const int64_t step = (int64_t)gridDim.x * q.rpc, row_first = (int64_t)blockIdx.x * q.rpc;
-    auto issue = [&](int64_t row0, int stage) {
-        const int64_t row = row0 + q.sub;
-        if (row < p.N) {
-            load_ahead<VPT, A>(ring, q, p.tpr, p.nv, stage, 0, p.x + row * p.H);
-            if (RES) load_ahead<VPT, A>(ring, q, p.tpr, p.nv, stage, A - 1, p.res + row * p.H);
+    const uint32_t base = smem_of(ring), stage_bytes = A * VPT * q.plane;
+    int64_t ahead = row_first + q.sub;  // the next row to load
+    const uint16_t *x = p.x + ahead * p.H, *res = RES ? p.res + ahead * p.H : nullptr;
+    const int64_t stride = step * p.H;
+    auto issue = [&](uint32_t at) {
+        if (ahead < p.N) {
+            load_ahead<VPT>(base + at, q, p.tpr, p.H, x);
+            if (RES) load_ahead<VPT>(base + at + VPT * q.plane, q, p.tpr, p.H, res);
         }
         cp_commit();
+        ahead += step;
+        x += stride;
+        if (RES) res += stride;
     };
     uint64_t g[VPT][8];
 #pragma unroll
     for (int j = 0; j < VPT; ++j)
         if (q.t + j * p.tpr < p.nv) load_gamma_pairs(p.gamma, p.gamma_fp32, (q.t + j * p.tpr) * kVec, g[j]);
 #pragma unroll
-    for (int s = 0; s < kDepth - 1; ++s) issue(row_first + s * step, s);
-    int stage = 0, flip = 0;
+    for (int s = 0; s < kDepth - 1; ++s) issue(s * stage_bytes);
+    uint32_t at = 0, fill = (kDepth - 1) * stage_bytes;
+    int flip = 0;
     for (int64_t row0 = row_first; row0 < p.N; row0 += step, flip ^= 1) {
         __syncwarp();  // the slot filled next was read by the whole group
-        issue(row0 + (kDepth - 1) * step, stage == 0 ? kDepth - 1 : stage - 1);
+        issue(fill);
+        fill = at;
         cp_wait<kDepth - 1>();
         __syncwarp();  // every lane's copies of this row are done
         const int64_t row = row0 + q.sub;
@@ -304,10 +313,10 @@ __global__ void __launch_bounds__(512) rmsnorm_stream_kernel(NormParams p) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[j][i] = 0;
             if (live && q.t + j * p.tpr < p.nv) {
-                read16<VPT, A>(ring, q, p.tpr, stage, 0, j, v[j]);
+                read16(ring + at + j * q.plane, q, v[j]);
                 if (RES) {
                     uint64_t r[8];
-                    read16<VPT, A>(ring, q, p.tpr, stage, A - 1, j, r);
+                    read16(ring + at + (VPT + j) * q.plane, q, r);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[j][i] = f32x2_add_rn(v[j][i], r[i]);
                 }
@@ -315,18 +324,19 @@ __global__ void __launch_bounds__(512) rmsnorm_stream_kernel(NormParams p) {
                 for (int i = 0; i < 8; ++i) ss = f32x2_fma_rn(v[j][i], v[j][i], ss);
             }
         }
-        const float rstd = 1.0f / sqrtf(stream_sum(ss, p.tpr, red[flip]) * p.inv_h + p.eps);
+        at = at == (kDepth - 1) * stage_bytes ? 0 : at + stage_bytes;
+        const float rstd = rsqrtf(stream_sum(ss, p.tpr, red[flip]) * p.inv_h + p.eps);
         if (live && q.t == 0 && p.rstd) p.rstd[row] = rstd;
         const uint64_t rr = f32x2_pack(rstd, rstd);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int k = q.t + j * p.tpr;
             const bool on = live && k < p.nv;
-            const int64_t at = row * p.H + k * kVec;
-            if (on && p.h) store16(p.h + at, v[j]);
+            const int64_t to = row * p.H + k * kVec;
+            if (on && p.h) store16(p.h + to, v[j]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[j][i] = f32x2_mul_rn(f32x2_mul_rn(v[j][i], rr), g[j][i]);
-            if (on && p.y) store16(p.y + at, v[j]);
+            if (on && p.y) store16(p.y + to, v[j]);
             if (p.q) {
                 float amax = 1e-4f;
                 if (on) {
@@ -348,12 +358,11 @@ __global__ void __launch_bounds__(512) rmsnorm_stream_kernel(NormParams p) {
                                      b = f32x2_unpack(f32x2_mul_rn(v[j][2 * i + 1], s2));
                         w[i] = pack_e4m3x2(a.x, a.y) | pack_e4m3x2(b.x, b.y) << 16;
                     }
-                    *reinterpret_cast<uint4*>(p.q + at) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4*>(p.q + to) = make_uint4(w[0], w[1], w[2], w[3]);
                     if ((k & 7) == 0) p.q_scale[row * (p.H / 128) + k / 8] = amax / 448.0f;
                 }
             }
         }
-        stage = stage == kDepth - 1 ? 0 : stage + 1;
     }
 }
 
@@ -451,19 +460,24 @@ __global__ void __launch_bounds__(1024) rmsnorm_bwd_kernel(NormBwdParams p) {
 // dgamma sums through shared memory, in row order, and writes one partial row.
 template <int VPT, bool DH>
 __global__ void __launch_bounds__(512) rmsnorm_bwd_stream_kernel(NormBwdParams p) {
-    extern __shared__ __align__(16) uint4 ring[];
+    extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float red[2][32];
     constexpr int A = DH ? 3 : 2, kDepth = depth_of(VPT, A);
     const Place q = place_of(p.tpr);
     const int64_t step = (int64_t)gridDim.x * q.rpc, row_first = (int64_t)blockIdx.x * q.rpc;
-    auto issue = [&](int64_t row0, int stage) {
-        const int64_t row = row0 + q.sub;
-        if (row < p.N) {
-            load_ahead<VPT, A>(ring, q, p.tpr, p.nv, stage, 0, p.h + row * p.H);
-            load_ahead<VPT, A>(ring, q, p.tpr, p.nv, stage, 1, p.dy + row * p.H);
-            if (DH) load_ahead<VPT, A>(ring, q, p.tpr, p.nv, stage, A - 1, p.dh + row * p.H);
+    const uint32_t base = smem_of(ring), stage_bytes = A * VPT * q.plane;
+    int64_t ahead = row_first + q.sub;  // the next row to load
+    int64_t from = ahead * p.H;
+    const int64_t stride = step * p.H;
+    auto issue = [&](uint32_t at) {
+        if (ahead < p.N) {
+            load_ahead<VPT>(base + at, q, p.tpr, p.H, p.h + from);
+            load_ahead<VPT>(base + at + VPT * q.plane, q, p.tpr, p.H, p.dy + from);
+            if (DH) load_ahead<VPT>(base + at + 2 * VPT * q.plane, q, p.tpr, p.H, p.dh + from);
         }
         cp_commit();
+        ahead += step;
+        from += stride;
     };
     uint64_t g[VPT][8], dg[VPT][8];
 #pragma unroll
@@ -473,12 +487,14 @@ __global__ void __launch_bounds__(512) rmsnorm_bwd_stream_kernel(NormBwdParams p
         for (int i = 0; i < 8; ++i) dg[j][i] = 0;
     }
 #pragma unroll
-    for (int s = 0; s < kDepth - 1; ++s) issue(row_first + s * step, s);
-    int stage = 0, flip = 0;
+    for (int s = 0; s < kDepth - 1; ++s) issue(s * stage_bytes);
+    uint32_t at = 0, fill = (kDepth - 1) * stage_bytes;
+    int flip = 0;
     float rstd_next = row_first + q.sub < p.N ? p.rstd[row_first + q.sub] : 0.f;
     for (int64_t row0 = row_first; row0 < p.N; row0 += step, flip ^= 1) {
         __syncwarp();  // the slot filled next was read by the whole group
-        issue(row0 + (kDepth - 1) * step, stage == 0 ? kDepth - 1 : stage - 1);
+        issue(fill);
+        fill = at;
         const int64_t row = row0 + q.sub;
         const bool live = row < p.N;
         const float rstd = rstd_next;
@@ -490,8 +506,8 @@ __global__ void __launch_bounds__(512) rmsnorm_bwd_stream_kernel(NormBwdParams p
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             if (live && q.t + j * p.tpr < p.nv) {
-                read16<VPT, A>(ring, q, p.tpr, stage, 0, j, n[j]);
-                read16<VPT, A>(ring, q, p.tpr, stage, 1, j, dt[j]);
+                read16(ring + at + j * q.plane, q, n[j]);
+                read16(ring + at + (VPT + j) * q.plane, q, dt[j]);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     n[j][i] = f32x2_mul_rn(n[j][i], rr);
@@ -509,7 +525,7 @@ __global__ void __launch_bounds__(512) rmsnorm_bwd_stream_kernel(NormBwdParams p
             if (live && k < p.nv) {
                 uint64_t o[8];
                 if (DH) {
-                    read16<VPT, A>(ring, q, p.tpr, stage, A - 1, j, o);
+                    read16(ring + at + (2 * VPT + j) * q.plane, q, o);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) o[i] = 0;
@@ -519,7 +535,7 @@ __global__ void __launch_bounds__(512) rmsnorm_bwd_stream_kernel(NormBwdParams p
                 store16(p.dx + row * p.H + k * kVec, o);
             }
         }
-        stage = stage == kDepth - 1 ? 0 : stage + 1;
+        at = at == (kDepth - 1) * stage_bytes ? 0 : at + stage_bytes;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     float* sums = reinterpret_cast<float*>(ring);  // [rpc][H]
