@@ -614,17 +614,17 @@ int64_t bwd_slots(int64_t N, int tpr) {
     return rows < most ? rows : most;
 }
 
-// CTAs that the device holds at once; 0 on an error.
-int resident(const void* kernel, int threads, int smem) {
-    int dev = 0, sms = 0, per = 0;
+// CTAs that the device holds at once (per SM, on its SMs); 0 on an error.
+int resident(const void* kernel, int threads, int smem, int* per, int* sms) {
+    int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, smem) != cudaSuccess) {
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(per, kernel, threads, smem) != cudaSuccess) {
         cudaGetLastError();
         return 0;
     }
-    return per * sms;
+    return *per * *sms;
 }
 
 ep_status_t check_shape(int64_t N, int H, int gamma_type) {
@@ -694,7 +694,13 @@ ep_status_t ep_rmsnorm(int64_t N, int H, const void* d_x, const void* d_residual
                                       : (ps.res ? rmsnorm_stream_kernel<2, true> : rmsnorm_stream_kernel<2, false>);
         const int64_t groups = (N + rps - 1) / rps;
         if (groups >= kStreamRows) {
-            const int ctas = resident((const void*)kernel, threads, smem);
+            int per = 0, sms = 0;
+            int ctas = resident((const void*)kernel, threads, smem, &per, &sms);
+            // HBM bounds a stream with a residual, and one CTA per SM then reads
+            // and writes faster than two (32768 x 7168: 6.44 against 5.57 TB/s);
+            // instructions bound one without (153 against 185 us), and the
+            // reduction's latency a few rows per SM.
+            if (per > 1 && ps.res && groups >= 16 * sms) ctas = sms;
             if (ctas > 0) {
                 kernel<<<(unsigned)(groups < ctas ? groups : ctas), threads, smem, s>>>(ps);
                 return launched("rmsnorm");
@@ -769,7 +775,8 @@ ep_status_t ep_rmsnorm_backward(int64_t N, int H, const void* d_h, const float* 
             svpt == 1 ? (ps.dh ? rmsnorm_bwd_stream_kernel<1, true> : rmsnorm_bwd_stream_kernel<1, false>)
                       : (ps.dh ? rmsnorm_bwd_stream_kernel<2, true> : rmsnorm_bwd_stream_kernel<2, false>);
         const int64_t groups = (N + rps - 1) / rps;
-        int64_t ctas = resident((const void*)kernel, threads, smem);
+        int per = 0, sms = 0;
+        int64_t ctas = resident((const void*)kernel, threads, smem, &per, &sms);
         if (ctas > kMaxSlots) ctas = kMaxSlots;
         if (groups < ctas) ctas = groups;
         if (ctas > 0) {
