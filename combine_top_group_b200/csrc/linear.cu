@@ -15,6 +15,7 @@
 //    and leaves it times its scales (row scale x weight block scale, fp32)
 //    into fp32 registers, since the scales differ from block to block.
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include <atomic>
@@ -85,9 +86,9 @@ constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarps + 3);  // + loads, products, e4m3 scales
 constexpr int kSub = 128 * 128;                 // bytes of a 128-channel weight tile of one stage
 constexpr int kMaxStages = 10;
-constexpr int kMaxBn = 128;
-// Shared memory: ring | staging (unsplit) | barriers and scales.
+// Shared memory: ring | staging, or inboxes | barriers and scales.
 constexpr int kStaging = 32 * 256 * 4;
+constexpr int kInbox = 2 * 36 * 256 * 4;        // a cluster's: 2 x at most 36 rows (splits x rows of each)
 constexpr int kMaxAcc = 8;                      // accumulator sets in tensor memory
 constexpr int kScales = 1024 * 4;               // [sets][2][bn]
 constexpr int kControl = 512 + kScales;
@@ -248,17 +249,18 @@ __device__ __forceinline__ bool epi_sync_and(bool ok) {
 }
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory"); }
 
-template <bool F8, bool SPLIT>
+// BN: rows of x per tile (p.bn).
+template <bool F8, bool SPLIT, int BN>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, LinearParams p) {
     extern __shared__ uint8_t smem_raw[];
-    const int sb = stage_bytes(p.na, p.bn);
+    const int sb = stage_bytes(p.na, BN);
     // swizzled tiles start on 1024 bytes (the same offset in every CTA of a cluster)
     const uint32_t ring = (tc::smem_u32(smem_raw) + 1023) & ~1023u;
     uint8_t* smem = smem_raw + (ring - tc::smem_u32(smem_raw));
     uint8_t* after = smem + (size_t)p.stages * sb;
-    float* staging = reinterpret_cast<float*>(SPLIT ? smem : after);
-    uint8_t* control = after + (SPLIT ? 0 : kStaging);
+    float* staging = reinterpret_cast<float*>(after);
+    uint8_t* control = after + (SPLIT ? kInbox : kStaging);
     float* scales = reinterpret_cast<float*>(control + 512);  // [sets][2][bn]
     volatile uint32_t* stop = reinterpret_cast<uint32_t*>(control + 500);
     const uint32_t bars = tc::smem_u32(control);
@@ -268,6 +270,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto acc_empty = [&](int s) { return bars + 8 * (2 * kMaxStages + kMaxAcc + s); };
     auto scale_full = [&](int s) { return bars + 8 * (2 * kMaxStages + 2 * kMaxAcc + s); };
     const uint32_t drained = bars + 8 * (2 * kMaxStages + 3 * kMaxAcc);
+    auto inbox_full = [&](int b) { return drained + 8 + 8 * b; };
+    auto inbox_free = [&](int b) { return drained + 24 + 8 * b; };
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(control + 496);
     const int sets = 1 << p.acc_log;
     // set of the acc-th use, the parity of that use's phase, and of the one before it
@@ -286,19 +290,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::bar_init(scale_full(s), 32);
         }
         tc::bar_init(drained, 1);
+        for (int b = 0; b < 2; ++b) {
+            tc::bar_init(inbox_full(b), 1);
+            tc::bar_init(inbox_free(b), p.splits);
+        }
         *stop = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kEpiWarps + 1) tc::tmem_alloc(tc::smem_u32(tmem_at), p.cols);
     tc::fence_before();
     __syncthreads();
+    if (SPLIT) tc::cluster_sync();
     tc::fence_after();
     const uint32_t tmem = *tmem_at;
 
+    // the CTAs of a cluster take the same tiles, each its part of in_features
     const int rank = SPLIT ? (int)tc::cluster_rank() : 0;
     const int first = SPLIT ? blockIdx.x / p.splits : blockIdx.x;
-    // a split launch has a cluster for each tile there can be
-    const int step = SPLIT ? 1 << 30 : gridDim.x;
+    const int step = SPLIT ? gridDim.x / p.splits : gridDim.x;
     const int k_lo = SPLIT ? (int)((int64_t)p.kblocks * rank / p.splits) : 0;
     const int k_hi = SPLIT ? (int)((int64_t)p.kblocks * (rank + 1) / p.splits) : p.kblocks;
     constexpr int kElems = F8 ? 128 : 64;  // in_features of a block
@@ -313,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (int id = first; ok && find_tile(p, cur, id, t); id += step) {
             const int subs = subs_of(p, t);
-            const uint32_t bytes = subs * kSub + p.bn * 128;
+            const uint32_t bytes = subs * kSub + BN * 128;
             for (int k = k_lo; k < k_hi; ++k, ++i) {
                 if (wrap > 0) ok = __all_sync(FULL, tc::bar_wait(empty(s), (wrap - 1) & 1, stop));
                 if (!ok) break;
@@ -351,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::fence_after();
                 const uint32_t at = ring + s * sb;
                 const uint64_t b = tc::smem_desc(at + p.na * kSub), w = tc::smem_desc(at);
-                const uint32_t d = tmem + set_of(acc) * p.na * p.bn;
+                const uint32_t d = tmem + set_of(acc) * p.na * BN;
                 const uint32_t keep = !F8 && k > k_lo ? 1u : 0u;
                 const bool last = F8 || k == k_hi - 1;
                 if (tc::elect()) {
@@ -361,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (subs == 2) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
-                            tc::mma<F8>(d + p.bn, w + kSub / 16 + 2 * q, b + 2 * q, idesc, q > 0 ? 1u : keep);
+                            tc::mma<F8>(d + BN, w + kSub / 16 + 2 * q, b + 2 * q, idesc, q > 0 ? 1u : keep);
                     }
                     tc::commit(empty(s));
                     if (last) tc::commit(acc_full(set_of(acc)));
@@ -392,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                          min(channel_of(p, t, a) / 128, nb - 1)) * p.kblocks;
                 // four blocks at a time, loaded four ahead: one load per block
                 // would hold each block up by its latency
-                float xn[kMaxBn / 32][4], wn[2][4];
+                float xn[BN / 32][4], wn[2][4];
                 auto fetch = [&](int k) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
@@ -400,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         wn[0][q] = in ? ws[0][k + q] : 0.f;
                         wn[1][q] = in && subs == 2 ? ws[1][k + q] : 0.f;
 #pragma unroll
-                        for (int j = 0; j < kMaxBn / 32; ++j)
+                        for (int j = 0; j < BN / 32; ++j)
                             xn[j][q] = in && lane + 32 * j < t.rows
                                            ? p.x_scale[(t.row + lane + 32 * j) * p.kblocks + k + q] : 0.f;
                     }
@@ -408,13 +417,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fetch(k_lo);
 #pragma unroll 1
                 for (int k = k_lo; ok && k < k_hi; k += 4) {
-                    float x4[kMaxBn / 32][4], w4[2][4];
+                    float x4[BN / 32][4], w4[2][4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         w4[0][q] = wn[0][q];
                         w4[1][q] = wn[1][q];
 #pragma unroll
-                        for (int j = 0; j < kMaxBn / 32; ++j) x4[j][q] = xn[j][q];
+                        for (int j = 0; j < BN / 32; ++j) x4[j][q] = xn[j][q];
                     }
                     fetch(k + 4);
 #pragma unroll
@@ -422,12 +431,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!ok || k + q >= k_hi) continue;
                         if (acc >= sets) ok = __all_sync(FULL, tc::bar_wait(acc_empty(set_of(acc)), phase_of(acc) ^ 1, stop));
                         if (!ok) continue;
-                        float* dst = scales + set_of(acc) * 2 * p.bn;
+                        float* dst = scales + set_of(acc) * 2 * BN;
 #pragma unroll
-                        for (int j = 0; j < kMaxBn / 32; ++j)
-                            if (32 * j < p.bn) {
+                        for (int j = 0; j < BN / 32; ++j)
+                            if (32 * j < BN) {
                                 dst[lane + 32 * j] = x4[j][q] * w4[0][q];
-                                dst[p.bn + lane + 32 * j] = x4[j][q] * w4[1][q];
+                                dst[BN + lane + 32 * j] = x4[j][q] * w4[1][q];
                             }
                         tc::bar_arrive(scale_full(set_of(acc)));
                         ++acc;
@@ -439,16 +448,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int sub = warp >> 2;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const int col = sub * 128 + (warp & 3) * 32 + lane;  // channel within a staged row
-        int acc = 0;
+        int acc = 0, use = 0;  // accumulator sets, inboxes
         bool ok = true;
         for (int id = first; ok && find_tile(p, cur, id, t); id += step) {
             const int subs = subs_of(p, t);
             Bias bias;
             load_bias(p, t, subs, bias);
-            uint64_t sum[F8 ? kMaxBn / 2 : 1];  // fp32 pairs: columns 2i, 2i + 1
+            uint64_t sum[F8 ? BN / 2 : 1];  // fp32 pairs: columns 2i, 2i + 1
             if (F8) {
 #pragma unroll
-                for (int i = 0; i < kMaxBn / 2; ++i) sum[i] = 0;
+                for (int i = 0; i < BN / 2; ++i) sum[i] = 0;
                 for (int k = k_lo; ok && k < k_hi; ++k, ++acc) {
                     ok = tc::bar_wait(acc_full(set_of(acc)), phase_of(acc), stop) &&
                          tc::bar_wait(scale_full(set_of(acc)), phase_of(acc), stop);
@@ -456,10 +465,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     tc::fence_after();
                     if (sub < subs) {
-                        const ulonglong2* sc = reinterpret_cast<const ulonglong2*>(scales + (set_of(acc) * 2 + sub) * p.bn);
-                        const uint32_t at = tmem + lane_base + (set_of(acc) * p.na + sub) * p.bn;
+                        const ulonglong2* sc = reinterpret_cast<const ulonglong2*>(scales + (set_of(acc) * 2 + sub) * BN);
+                        const uint32_t at = tmem + lane_base + (set_of(acc) * p.na + sub) * BN;
 #pragma unroll
-                        for (int c = 0; c < kMaxBn / 32; ++c) {
+                        for (int c = 0; c < BN / 32; ++c) {
                             if (c * 32 >= t.rows) continue;
                             uint32_t v[32];
                             tc::tmem_ld32(at + c * 32, v);
@@ -484,32 +493,73 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = __all_sync(FULL, tc::bar_wait(acc_full(set_of(acc)), phase_of(acc), stop));
                 tc::fence_after();
             }
+            const uint32_t at = tmem + lane_base + (set_of(acc) * p.na + sub) * BN;
+            const int width = subs * 128;
             // all warps leave after the same tile: none may wait below for one that left
             ok = epi_sync_and(ok);
-            const uint32_t at = tmem + lane_base + (set_of(acc) * p.na + sub) * p.bn;
-            const int width = subs * 128;
 #pragma unroll
-            for (int c = 0; c < kMaxBn / 32; ++c) {
+            for (int c = 0; c < BN / 32; ++c) {
                 if (c * 32 >= t.rows) continue;
-                if (!SPLIT && c > 0) epi_sync();  // staging is free
-                float* row0 = staging + (SPLIT ? c * 32 * width : 0) + col;
-                if (ok && sub < subs) {
-                    if (F8) {
+                uint32_t v[32];
+                if (F8) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const float2 v = f32x2_unpack(sum[F8 ? c * 16 + j : 0]);
-                            row0[(2 * j) * width] = v.x;
-                            row0[(2 * j + 1) * width] = v.y;
+                    for (int j = 0; j < 16; ++j) {
+                        const float2 f = f32x2_unpack(sum[F8 ? c * 16 + j : 0]);
+                        v[2 * j] = __float_as_uint(f.x);
+                        v[2 * j + 1] = __float_as_uint(f.y);
+                    }
+                } else if (ok && sub < subs) {
+                    tc::tmem_ld32(at + c * 32, v);
+                    tc::tmem_ld_wait();
+                }
+                if (SPLIT) {
+                    // Row r of the chunk belongs to CTA r % splits. All CTAs push
+                    // their sums of it into that one's inbox, which adds them in
+                    // the order of the CTAs. Two inboxes alternate.
+                    const int b = use & 1, rows = min(32, t.rows - c * 32);
+                    const int slots = (32 + p.splits - 1) / p.splits;  // rows of a CTA, at most
+                    if (use >= 2) ok = tc::bar_wait(inbox_free(b), (use / 2 - 1) & 1, stop) && ok;
+                    if (threadIdx.x == 0)
+                        tc::bar_expect(inbox_full(b), (rows + p.splits - 1 - rank) / p.splits * p.splits * width * 4);
+                    if (ok && sub < subs) {
+                        const uint32_t to =
+                            tc::smem_u32(staging) + b * (kInbox / 2) + (rank * slots * width + col) * 4;
+                        int owner = 0, slot = 0;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            if (j < rows)
+                                tc::push(tc::peer_smem(to + slot * width * 4, owner), v[j],
+                                         tc::peer_smem(inbox_full(b), owner));
+                            if (++owner == p.splits) {
+                                owner = 0;
+                                ++slot;
+                            }
                         }
-                    } else {
-                        uint32_t v[32];
-                        tc::tmem_ld32(at + c * 32, v);
-                        tc::tmem_ld_wait();
+                    }
+                    ok = tc::bar_wait(inbox_full(b), (use / 2) & 1, stop) && ok;
+                    ok = epi_sync_and(ok);
+                    const float* box = staging + b * (kInbox / 8);
+                    if (ok)
+                        for (int i = warp; rank + i * p.splits < rows; i += kEpiWarps)
+                            emit_row(p, t, subs, bias, t.row + c * 32 + rank + i * p.splits, [&](int s) {
+                                const float* from = box + i * width + s * 128 + lane * 4;
+                                float4 a = *reinterpret_cast<const float4*>(from);
+                                for (int q = 1; q < p.splits; ++q) {
+                                    const float4 w = *reinterpret_cast<const float4*>(from + q * slots * width);
+                                    a = make_float4(a.x + w.x, a.y + w.y, a.z + w.z, a.w + w.w);
+                                }
+                                return a;
+                            });
+                    epi_sync();
+                    if (threadIdx.x < p.splits) tc::bar_arrive_at(tc::peer_smem(inbox_free(b), threadIdx.x));
+                    ++use;
+                } else {
+                    if (c > 0) epi_sync();  // staging is free
+                    float* row0 = staging + col;
+                    if (ok && sub < subs) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j) row0[j * width] = __uint_as_float(v[j]);
                     }
-                }
-                if (!SPLIT) {
                     epi_sync();
                     if (ok)
                         for (int r = warp; r < 32 && c * 32 + r < t.rows; r += kEpiWarps)
@@ -526,33 +576,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     }
-    if (SPLIT) {
-        // every CTA of the cluster holds its part of the tile's sums in
-        // staging (its products, and so its ring, are done); rows go round
-        __syncwarp();
-        tc::cluster_sync();
-        Cursor c2;
-        if (!*stop && warp < kEpiWarps && find_tile(p, c2, first, t)) {
-            const int subs = subs_of(p, t), width = subs * 128;
-            Bias bias;
-            load_bias(p, t, subs, bias);
-            const uint32_t mine = tc::smem_u32(staging);
-            for (int r = rank + warp * p.splits; r < t.rows; r += kEpiWarps * p.splits)
-                emit_row(p, t, subs, bias, t.row + r, [&](int s) {
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int q = 0; q < p.splits; ++q) {
-                        const float4 w = tc::ld_peer(tc::peer_smem(mine + (r * width + s * 128 + lane * 4) * 4, q));
-                        v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
-                    }
-                    return v;
-                });
-        }
-        __syncwarp();
-        tc::cluster_sync();
-    } else {
-        __syncwarp();
-        __syncthreads();
-    }
+    __syncwarp();
+    __syncthreads();
+    if (SPLIT) tc::cluster_sync();  // no CTA leaves while another may push into its inbox
     if (threadIdx.x == 0 && *stop) set_error(p.err, EP_DEVERR_TIMEOUT);
     if (warp == kEpiWarps + 1) tc::tmem_free(tmem, p.cols);
 }
@@ -986,6 +1012,12 @@ LinearParams params_of(const ep_linear_t& q) {
 
 constexpr int kMaxSplits = 8;
 
+template <bool F8>
+auto kernel_of(bool split, int bn) {
+    if (split) return bn == 32 ? linear_kernel<F8, true, 32> : bn == 64 ? linear_kernel<F8, true, 64> : linear_kernel<F8, true, 128>;
+    return bn == 32 ? linear_kernel<F8, false, 32> : bn == 64 ? linear_kernel<F8, false, 64> : linear_kernel<F8, false, 128>;
+}
+
 // Clusters of n CTAs, one CTA per SM, that device b can hold at once: fewer
 // than SMs / n, since a cluster stays within a GPC (15 of 8, not 18).
 int clusters_of(const ep_buffer& b, int n) {
@@ -1003,7 +1035,7 @@ int clusters_of(const ep_buffer& b, int n) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const auto kernel = linear_kernel<false, true>;
+    const auto kernel = linear_kernel<false, true, 128>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) != cudaSuccess ||
         cudaOccupancyMaxActiveClusters(&count, kernel, &cfg) != cudaSuccess) {
         cudaGetLastError();
@@ -1021,10 +1053,11 @@ struct Shape {
 };
 
 // Takes the kernel with the least time by this estimate, in microseconds for
-// 128 bytes of in_features: 0.28 (bf16) or 0.88 (e4m3) for a pair's 256 x 256
-// tile; 0.50 or 1.34 for a CTA's 128 rows x 256 channels, 0.28 where its rows
-// are few (it then waits for weights alone). An expert's last tile is half
-// empty in the mean: of 256 rows with pairs, of 16 columns without.
+// 128 bytes of in_features, as measured on large layers: 0.28 (bf16) or 0.88
+// (e4m3) for a pair's 256 x 256 tile; 0.50 or 1.34 for a CTA's 128 rows x 256
+// channels, half of that with 128 channels, and 0.28 or 0.45 where its rows are
+// few (it then waits for weights). With pairs an expert's last tile is half
+// empty in the mean.
 Shape shape_of(const ep_buffer& b, const LinearParams& p, int64_t avg, int64_t most) {
     const bool f8 = p.x_scale != nullptr;
     const int64_t groups = most < p.G ? most : p.G;
@@ -1040,16 +1073,27 @@ Shape shape_of(const ep_buffer& b, const LinearParams& p, int64_t avg, int64_t m
         c.na = 1;
         c.nt = (p.N + 127) / 128;
     }
-    // few tiles: a cluster shares each, as many CTAs as the device can hold clusters of
+    // A cluster can share each tile's in_features: n CTAs finish a tile n times
+    // as fast, less the exchange of its sums, and rounds over all tiles come
+    // out less ragged. The exchange takes 2 us.
     c.splits = 1;
-    for (int n = 2; n <= kMaxSplits; ++n)
-        if (likely * c.nt <= clusters_of(b, n) && p.kblocks >= 4 * n && c.bound * c.nt * n <= 4 * b.sm_count) c.splits = n;
+    const double block = c.bn < 128 ? (f8 ? 0.45 : 0.28) : (f8 ? 0.67 : 0.25) * c.na;
+    double best = 0;
+    for (int n = 1; n <= kMaxSplits && p.kblocks >= 4 * n; ++n) {
+        const int64_t at_once = n == 1 ? b.sm_count : clusters_of(b, n);
+        if (at_once < 1) continue;
+        const int64_t rounds = (likely * c.nt + at_once - 1) / at_once;
+        const double time = rounds * ((p.kblocks + n - 1) / n * block + (n > 1 ? 2.0 : 0.5));
+        if (n == 1 || time < best) {
+            best = time;
+            c.splits = n;
+        }
+    }
     if (avg < 256 || p.wide < 256) return c;
-    const double rounds_c = (double)likely * c.nt / b.sm_count, rounds_p =
-        (p.G == 1 ? (double)tiles(256) : groups * (avg / 256.0 + 0.5)) * ((p.wide + 255) / 256) / (b.sm_count / 2);
-    const double time_c = (rounds_c < 1 ? 1.0 / c.splits : rounds_c) * (f8 ? 1.34 : 0.50) * c.na / 2;
-    const double time_p = (rounds_p < 1 ? 1.0 : rounds_p) * (f8 ? 0.88 : 0.28);
-    if (time_p > time_c) return c;
+    double rounds_p = (p.G == 1 ? (double)tiles(256) : groups * (avg / 256.0 + 0.5)) * ((p.wide + 255) / 256) / (b.sm_count / 2);
+    if (rounds_p < 4) rounds_p = ceil(rounds_p);
+    const double time_p = rounds_p * p.kblocks * (f8 ? 0.88 : 0.28);
+    if (time_p > best) return c;
     c.pair = true;
     c.bn = 256;
     c.na = 2;
@@ -1077,10 +1121,9 @@ ep_status_t launch_on_device(const ep_buffer& b, LinearParams p, int64_t x_rows,
     if (bound * p.nt >= (int64_t)1 << 30) return fail(EP_ERR_UNSUPPORTED, "too many tiles: rows x out_features");
     const bool split = p.splits > 1;
     const int sb = stage_bytes(p.na, p.bn);
-    const int fixed = kControl + (split ? 0 : kStaging) + 1024;  // 1024: alignment of the ring
+    const int fixed = kControl + (split ? kInbox : kStaging) + 1024;  // 1024: alignment of the ring
     p.stages = (kSmemMax - fixed) / sb;
     if (p.stages > kMaxStages) p.stages = kMaxStages;
-    // a split CTA stages its whole tile in the ring
     const int smem = p.stages * sb + fixed;
     // bf16 fills one set while another is read; e4m3 hands a set over for each
     // block, and more of them hide the hand-over
@@ -1097,13 +1140,13 @@ ep_status_t launch_on_device(const ep_buffer& b, LinearParams p, int64_t x_rows,
     if (!encode(&map_x, f8, p.x, 2, dx, sx, pair ? 128 : p.bn) || !encode(&map_w, f8, p.w, 4, dw, sw, 128))
         return fail(EP_ERR_UNSUPPORTED, "x or w is too large for a tensor map");
 
-    auto kernel = pair ? (f8 ? linear_pair_kernel<true> : linear_pair_kernel<false>) : split ? (f8 ? linear_kernel<true, true> : linear_kernel<false, true>)
-                        : (f8 ? linear_kernel<true, false> : linear_kernel<false, false>);
+    const auto kernel = pair ? (f8 ? linear_pair_kernel<true> : linear_pair_kernel<false>)
+                        : f8 ? kernel_of<true>(split, p.bn) : kernel_of<false>(split, p.bn);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
     if (e != cudaSuccess) return fail(EP_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-    const int64_t tiles = bound * p.nt, pairs = b.sm_count / 2;
+    const int64_t tiles = bound * p.nt, pairs = b.sm_count / 2, clusters = split ? clusters_of(b, p.splits) : 0;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(pair ? 2 * (tiles < pairs ? tiles : pairs) : split ? tiles * p.splits : tiles < b.sm_count ? tiles : b.sm_count));
+    cfg.gridDim = dim3((unsigned)(pair ? 2 * (tiles < pairs ? tiles : pairs) : split ? p.splits * (tiles < clusters ? tiles : clusters) : tiles < b.sm_count ? tiles : b.sm_count));
     cfg.blockDim = dim3(pair ? kPairThreads : kThreads);
     cfg.dynamicSmemBytes = pair ? kPairSmem : smem;
     cfg.stream = stream;

@@ -222,12 +222,12 @@ __device__ __forceinline__ uint32_t peer_smem(uint32_t addr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-__device__ __forceinline__ float4 ld_peer(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr));
-    return v;
+// Stores into another CTA's shared memory; the bytes count towards the phase of
+// `bar` in that CTA, whose waiters then see the value.
+__device__ __forceinline__ void push(uint32_t addr, uint32_t value, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr), "r"(value),
+                 "r"(bar)
+                 : "memory");
 }
 
 }  // namespace tc
