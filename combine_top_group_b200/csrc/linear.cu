@@ -10,10 +10,15 @@
 // One persistent CTA per SM: a warp loads tiles with TMA into a ring of shared
 // memory stages, a warp issues the products, eight warps read finished
 // accumulators out of tensor memory, where a second set fills meanwhile.
-//  - bf16: the whole sum over in_features stays in tensor memory.
 //  - e4m3: each block of 128 channels is summed on its own in tensor memory
 //    and leaves it times its scales (row scale x weight block scale, fp32)
 //    into fp32 registers, since the scales differ from block to block.
+//  - bf16: the whole sum, or for fp32 and e4m3 outputs every 8 blocks of 64
+//    channels, leaves tensor memory the same way. Sums there lose about 1.5e-8
+//    of their size with each step of 16 channels (they are cut, not rounded:
+//    7e-6 over 7168 channels). That is nothing beside a bf16 output's 2^-8; 32
+//    steps keep it below the roundings of an fp32 sum of that length (4.8e-7
+//    measured for 512 to 7168 channels), at the price of 8 to 20% of the time.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -55,6 +60,7 @@ struct LinearParams {
     int stages;    // of the shared-memory ring
     int kblocks;   // 128-byte blocks of in_features
     int splits;    // CTAs of a cluster that share a tile's in_features
+    int flush;     // blocks summed in tensor memory at a time
     int acc_log;   // log2 of the accumulator sets
     uint32_t cols; // tensor-memory columns
     int vec;       // rows of out and residual allow 4-channel accesses
@@ -83,7 +89,12 @@ __device__ __forceinline__ float activate(int act, float z) {
 
 
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 32 * (kEpiWarps + 3);  // + loads, products, e4m3 scales
+// Three warpgroups: two of the epilogue, one of loads, products, e4m3 scales
+// and an idle warp. The launch gives each thread 168 registers; the epilogue's
+// fp32 sums need more: 2 * 128 * 216 + 128 * 72 = 384 * 168.
+constexpr int kThreads = 384;
+constexpr int kEpiRegs = 216, kOtherRegs = 72;
+static_assert(2 * 128 * kEpiRegs + 128 * kOtherRegs == kThreads * 168, "register split");
 constexpr int kSub = 128 * 128;                 // bytes of a 128-channel weight tile of one stage
 constexpr int kMaxStages = 10;
 // Shared memory: ring | staging, or inboxes | barriers and scales.
@@ -317,6 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The loads and products warps run their loops whole and converged; one
     // elected lane issues.
     if (warp == kEpiWarps) {  // loads
+        tc::fewer_registers<kOtherRegs>();
         int i = 0, s = 0;
         uint32_t wrap = 0;
         bool ok = true;
@@ -346,14 +358,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc::bar_drain(full(j % p.stages), (j / p.stages) & 1);
         }
     } else if (warp == kEpiWarps + 1) {  // products
+        tc::fewer_registers<kOtherRegs>();
         int s = 0, acc = 0;
         uint32_t wrap = 0;
         bool ok = true;
         for (int id = first; ok && find_tile(p, cur, id, t); id += step) {
             const int subs = subs_of(p, t);
             const uint32_t idesc = tc::instr_desc(F8, 128, (t.rows + 15) / 16 * 16);
+            int in_set = 0;  // blocks summed in this set so far
             for (int k = k_lo; k < k_hi; ++k) {
-                if ((F8 || k == k_lo) && acc >= sets)
+                if (in_set == 0 && acc >= sets)
                     ok = __all_sync(FULL, tc::bar_wait(acc_empty(set_of(acc)), phase_of(acc) ^ 1, stop));
                 if (ok) ok = __all_sync(FULL, tc::bar_wait(full(s), wrap & 1, stop));
                 if (!ok) break;
@@ -361,8 +375,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t at = ring + s * sb;
                 const uint64_t b = tc::smem_desc(at + p.na * kSub), w = tc::smem_desc(at);
                 const uint32_t d = tmem + set_of(acc) * p.na * BN;
-                const uint32_t keep = !F8 && k > k_lo ? 1u : 0u;
-                const bool last = F8 || k == k_hi - 1;
+                const uint32_t keep = in_set > 0 ? 1u : 0u;
+                const bool last = F8 || in_set == p.flush - 1 || k == k_hi - 1;
                 if (tc::elect()) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q)  // 32 bytes of K each
@@ -377,6 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
                 acc += last;
+                    in_set = last ? 0 : in_set + 1;
                 if (++s == p.stages) {
                     s = 0;
                     ++wrap;
@@ -388,6 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp == kEpiWarps + 2) {  // e4m3: row scale x weight block scale of each block and column
+        tc::fewer_registers<kOtherRegs>();
         if (F8) {
             int acc = 0;
             bool ok = true;
@@ -444,7 +460,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-    } else {  // epilogue: warps 0-3 read sub-tile 0, warps 4-7 sub-tile 1
+    } else if (warp < kEpiWarps) {  // epilogue: warps 0-3 read sub-tile 0, warps 4-7 sub-tile 1
+        tc::more_registers<kEpiRegs>();
         const int sub = warp >> 2;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const int col = sub * 128 + (warp & 3) * 32 + lane;  // channel within a staged row
@@ -454,46 +471,42 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int subs = subs_of(p, t);
             Bias bias;
             load_bias(p, t, subs, bias);
-            uint64_t sum[F8 ? BN / 2 : 1];  // fp32 pairs: columns 2i, 2i + 1
-            if (F8) {
+            uint64_t sum[BN / 2];  // fp32 pairs: columns 2i, 2i + 1
 #pragma unroll
-                for (int i = 0; i < BN / 2; ++i) sum[i] = 0;
-                for (int k = k_lo; ok && k < k_hi; ++k, ++acc) {
-                    ok = tc::bar_wait(acc_full(set_of(acc)), phase_of(acc), stop) &&
-                         tc::bar_wait(scale_full(set_of(acc)), phase_of(acc), stop);
-                    ok = __all_sync(FULL, ok);
-                    if (!ok) break;
-                    tc::fence_after();
-                    if (sub < subs) {
-                        const ulonglong2* sc = reinterpret_cast<const ulonglong2*>(scales + (set_of(acc) * 2 + sub) * BN);
-                        const uint32_t at = tmem + lane_base + (set_of(acc) * p.na + sub) * BN;
+            for (int i = 0; i < BN / 2; ++i) sum[i] = 0;
+            for (int k = k_lo; ok && k < k_hi; k += F8 ? 1 : p.flush, ++acc) {
+                ok = tc::bar_wait(acc_full(set_of(acc)), phase_of(acc), stop);
+                if (F8) ok = ok && tc::bar_wait(scale_full(set_of(acc)), phase_of(acc), stop);
+                ok = __all_sync(FULL, ok);
+                if (!ok) break;
+                tc::fence_after();
+                if (sub < subs) {
+                    const ulonglong2* sc = reinterpret_cast<const ulonglong2*>(scales + (set_of(acc) * 2 + sub) * BN);
+                    const uint32_t at = tmem + lane_base + (set_of(acc) * p.na + sub) * BN;
+                    const uint64_t one = f32x2_pack(1.f, 1.f);
 #pragma unroll
-                        for (int c = 0; c < BN / 32; ++c) {
-                            if (c * 32 >= t.rows) continue;
-                            uint32_t v[32];
-                            tc::tmem_ld32(at + c * 32, v);
-                            tc::tmem_ld_wait();
+                    for (int c = 0; c < BN / 32; ++c) {
+                        if (c * 32 >= t.rows) continue;
+                        uint32_t v[32];
+                        tc::tmem_ld32(at + c * 32, v);
+                        tc::tmem_ld_wait();
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const ulonglong2 s2 = sc[c * 8 + j];
-                                sum[c * 16 + 2 * j] = f32x2_fma_rn(
-                                    f32x2_pack(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1])), s2.x,
-                                    sum[c * 16 + 2 * j]);
-                                sum[c * 16 + 2 * j + 1] = f32x2_fma_rn(
-                                    f32x2_pack(__uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3])), s2.y,
-                                    sum[c * 16 + 2 * j + 1]);
-                            }
+                        for (int j = 0; j < 8; ++j) {
+                            ulonglong2 s2 = make_ulonglong2(one, one);
+                            if (F8) s2 = sc[c * 8 + j];
+                            sum[c * 16 + 2 * j] =
+                                f32x2_fma_rn(f32x2_pack(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1])), s2.x,
+                                             sum[c * 16 + 2 * j]);
+                            sum[c * 16 + 2 * j + 1] =
+                                f32x2_fma_rn(f32x2_pack(__uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3])),
+                                             s2.y, sum[c * 16 + 2 * j + 1]);
                         }
                     }
-                    tc::fence_before();
-                    __syncwarp();
-                    if (lane == 0) tc::bar_arrive(acc_empty(set_of(acc)));
                 }
-            } else {
-                ok = __all_sync(FULL, tc::bar_wait(acc_full(set_of(acc)), phase_of(acc), stop));
-                tc::fence_after();
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) tc::bar_arrive(acc_empty(set_of(acc)));
             }
-            const uint32_t at = tmem + lane_base + (set_of(acc) * p.na + sub) * BN;
             const int width = subs * 128;
             // all warps leave after the same tile: none may wait below for one that left
             ok = epi_sync_and(ok);
@@ -501,16 +514,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < BN / 32; ++c) {
                 if (c * 32 >= t.rows) continue;
                 uint32_t v[32];
-                if (F8) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float2 f = f32x2_unpack(sum[F8 ? c * 16 + j : 0]);
-                        v[2 * j] = __float_as_uint(f.x);
-                        v[2 * j + 1] = __float_as_uint(f.y);
-                    }
-                } else if (ok && sub < subs) {
-                    tc::tmem_ld32(at + c * 32, v);
-                    tc::tmem_ld_wait();
+                for (int j = 0; j < 16; ++j) {
+                    const float2 f = f32x2_unpack(sum[c * 16 + j]);
+                    v[2 * j] = __float_as_uint(f.x);
+                    v[2 * j + 1] = __float_as_uint(f.y);
                 }
                 if (SPLIT) {
                     // Row r of the chunk belongs to CTA r % splits. All CTAs push
@@ -568,13 +576,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             });
                 }
             }
-            if (!F8) {
-                tc::fence_before();
-                __syncwarp();
-                if (lane == 0) tc::bar_arrive(acc_empty(set_of(acc)));
-                ++acc;
-            }
         }
+    } else {
+        tc::fewer_registers<kOtherRegs>();
     }
     __syncwarp();
     __syncthreads();
@@ -593,12 +597,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // thread owns a row: its e4m3 scale is one register, and the epilogue needs no
 // exchange but the amax of an e4m3 row between two warps.
 
-// Three warpgroups: two of the epilogue, one of loads, products and two idle
-// warps. The launch gives each thread 168 registers; the epilogue's fp32 sums
-// need more: 2 * 128 * 224 + 128 * 56 = 384 * 168.
-constexpr int kPairThreads = 384;
-constexpr int kEpiRegs = 224, kOtherRegs = 56;
-static_assert(2 * 128 * kEpiRegs + 128 * kOtherRegs == kPairThreads * 168, "register split");
+constexpr int kPairEpiRegs = 224, kPairOtherRegs = 56;  // as kEpiRegs and kOtherRegs: no e4m3 scales warp here
+static_assert(2 * 128 * kPairEpiRegs + 128 * kPairOtherRegs == kThreads * 168, "register split");
 constexpr int kPairStage = 2 * kSub;
 constexpr int kPairStages = 6;
 constexpr int kPairSmem = kPairStages * kPairStage + 256 + 2 * 128 * 4 + 1024;
@@ -691,8 +691,10 @@ __device__ __forceinline__ void finish32(const LinearParams& p, int g, int64_t r
     }
 }
 
-template <bool F8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+// SUM: the sums leave tensor memory in parts, into registers; otherwise whole,
+// by the chunk that the epilogue works on (p.flush is then kblocks).
+template <bool F8, bool SUM>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                        LinearParams p) {
     extern __shared__ uint8_t smem_raw[];
@@ -734,7 +736,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     Tile t;
 
     if (warp == kEpiWarps) {  // loads, each CTA its halves
-        tc::fewer_registers<kOtherRegs>();
+        tc::fewer_registers<kPairOtherRegs>();
         int i = 0, s = 0;
         uint32_t wrap = 0;
         bool ok = true;
@@ -760,15 +762,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     tc::bar_drain(full(j % kPairStages), (j / kPairStages) & 1);
         }
     } else if (warp == kEpiWarps + 1) {  // products, by the leader
-        tc::fewer_registers<kOtherRegs>();
+        tc::fewer_registers<kPairOtherRegs>();
         if (rank == 0) {
             int s = 0, acc = 0;
             uint32_t wrap = 0;
             bool ok = true;
             const uint32_t idesc = tc::instr_desc(F8, 256, 256);
             for (int id = first; ok && find_tile(p, cur, id, t); id += step) {
+                int in_set = 0;  // blocks summed in this set so far
                 for (int k = 0; k < p.kblocks; ++k) {
-                    if ((F8 || k == 0) && acc >= 2)
+                    if (in_set == 0 && acc >= 2)
                         ok = __all_sync(FULL, tc::bar_wait(acc_empty(acc & 1), (acc / 2 - 1) & 1, stop));
                     if (ok) ok = __all_sync(FULL, tc::bar_wait(full(s), wrap & 1, stop));
                     if (!ok) break;
@@ -776,8 +779,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     const uint32_t at = ring + s * kPairStage;
                     const uint64_t a = tc::smem_desc(at), w = tc::smem_desc(at + kSub);
                     const uint32_t d = tmem + (acc & 1) * 256;
-                    const uint32_t keep = !F8 && k > 0 ? 1u : 0u;
-                    const bool last = F8 || k == p.kblocks - 1;
+                    const uint32_t keep = in_set > 0 ? 1u : 0u;
+                    const bool last = F8 || in_set == p.flush - 1 || k == p.kblocks - 1;
                     if (tc::elect()) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q)  // 32 bytes of K each
@@ -787,6 +790,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     }
                     __syncwarp();
                     acc += last;
+                    in_set = last ? 0 : in_set + 1;
                     if (++s == kPairStages) {
                         s = 0;
                         ++wrap;
@@ -799,7 +803,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             }
         }
     } else if (warp < kEpiWarps) {  // epilogue: warps w and w + 4 share 32 rows, half of the channels each
-        tc::more_registers<kEpiRegs>();
+        tc::more_registers<kPairEpiRegs>();
         const int half = warp >> 2;
         const int r = (warp & 3) * 32 + lane;  // row of the CTA's 128
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
@@ -815,10 +819,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             const bool live = r < rows;
             const int g = t.group / p.R;
             const int n0 = gated ? t.n * 128 + half * 64 : t.n * 256 + half * 128;  // the thread's first channel
-            uint64_t sum[F8 ? 64 : 1];  // fp32 pairs: 32 columns of each chunk
-            if (F8) {
+            uint64_t sum[SUM ? 64 : 1];  // fp32 pairs: 32 columns of each chunk
 #pragma unroll
-                for (int i = 0; i < 64; ++i) sum[i] = 0;
+            for (int i = 0; i < (SUM ? 64 : 1); ++i) sum[i] = 0;
+            // a set's sums, times p0 (first two chunks) or p1, from tensor memory
+            auto take = [&](uint64_t p0, uint64_t p1) {
+                tc::fence_after();
+                if (rows > (warp & 3) * 32) {
+                    const uint32_t at = tmem + lane_base + (acc & 1) * 256;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t v[32];
+                        tc::tmem_ld32(at + column(c), v);
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            sum[SUM ? c * 16 + j : 0] = f32x2_fma_rn(
+                                f32x2_pack(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])),
+                                c < 2 ? p0 : p1, sum[SUM ? c * 16 + j : 0]);
+                    }
+                }
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) tc::bar_arrive_at(empty_at[acc & 1]);
+                ++acc;
+            };
+            if (F8) {
                 const int nb = (p.N + 127) / 128;
                 const float* xs = p.x_scale + (live ? row : t.row) * p.kblocks;
                 const float* w0 = p.w_scale + ((int64_t)g * p.parts * nb + (gated ? t.n : min(t.n * 2 + half, nb - 1))) * p.kblocks;
@@ -841,46 +867,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         const float s0 = x4[q] * w0[k0 + q], s1 = x4[q] * w1[k0 + q];
                         ok = __all_sync(FULL, tc::bar_wait(acc_full(acc & 1), (acc / 2) & 1, stop));
                         if (!ok) continue;
-                        tc::fence_after();
-                        if (rows > (warp & 3) * 32) {
-                            const uint32_t at = tmem + lane_base + (acc & 1) * 256;
-                            const uint64_t p0 = f32x2_pack(s0, s0), p1 = f32x2_pack(s1, s1);
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                uint32_t v[32];
-                                tc::tmem_ld32(at + column(c), v);
-                                tc::tmem_ld_wait();
-#pragma unroll
-                                for (int j = 0; j < 16; ++j)
-                                    sum[c * 16 + j] = f32x2_fma_rn(
-                                        f32x2_pack(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])),
-                                        c < 2 ? p0 : p1, sum[c * 16 + j]);
-                            }
-                        }
-                        tc::fence_before();
-                        __syncwarp();
-                        if (lane == 0) tc::bar_arrive_at(empty_at[acc & 1]);
-                        ++acc;
+                        take(f32x2_pack(s0, s0), f32x2_pack(s1, s1));
                     }
                 }
-            } else {
+            } else if (!SUM) {
                 ok = __all_sync(FULL, tc::bar_wait(acc_full(acc & 1), (acc / 2) & 1, stop));
                 tc::fence_after();
+            } else {
+                const uint64_t one = f32x2_pack(1.f, 1.f);
+                for (int k = 0; k < p.kblocks; k += p.flush) {
+                    ok = __all_sync(FULL, tc::bar_wait(acc_full(acc & 1), (acc / 2) & 1, stop));
+                    if (!ok) break;
+                    take(one, one);
+                }
             }
             // all warps leave after the same tile: none may wait below for one that left
             ok = epi_sync_and(ok);
-            const uint32_t at = tmem + lane_base + (acc & 1) * 256;
             auto load = [&](int c, float(&z)[32]) {
-                if (F8) {
+                if (SUM) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        const float2 v = f32x2_unpack(sum[F8 ? c * 16 + j : 0]);
+                        const float2 v = f32x2_unpack(sum[SUM ? c * 16 + j : 0]);
                         z[2 * j] = v.x;
                         z[2 * j + 1] = v.y;
                     }
                 } else {
                     uint32_t v[32];
-                    tc::tmem_ld32(at + column(c), v);
+                    tc::tmem_ld32(tmem + lane_base + (acc & 1) * 256 + column(c), v);
                     tc::tmem_ld_wait();
 #pragma unroll
                     for (int j = 0; j < 32; ++j) z[j] = __uint_as_float(v[j]);
@@ -917,7 +930,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     }
                 }
             }
-            if (!F8) {
+            if (!SUM) {
                 tc::fence_before();
                 __syncwarp();
                 if (lane == 0) tc::bar_arrive_at(empty_at[acc & 1]);
@@ -925,7 +938,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             }
         }
     } else {
-        tc::fewer_registers<kOtherRegs>();
+        tc::fewer_registers<kPairOtherRegs>();
     }
     __syncwarp();
     __syncthreads();
@@ -1111,6 +1124,7 @@ ep_status_t launch_on_device(const ep_buffer& b, LinearParams p, int64_t x_rows,
     const int size = f8 ? 1 : 2;
     p.kblocks = f8 ? p.K / 128 : (p.K + 63) / 64;
     p.vec = p.N % 4 == 0;
+    p.flush = f8 ? 1 : p.out_type == EP_DTYPE_BF16 ? p.kblocks : 8;
     const Shape c = shape_of(b, p, avg, most);
     const bool pair = c.pair;
     p.bn = c.bn;
@@ -1125,9 +1139,9 @@ ep_status_t launch_on_device(const ep_buffer& b, LinearParams p, int64_t x_rows,
     p.stages = (kSmemMax - fixed) / sb;
     if (p.stages > kMaxStages) p.stages = kMaxStages;
     const int smem = p.stages * sb + fixed;
-    // bf16 fills one set while another is read; e4m3 hands a set over for each
-    // block, and more of them hide the hand-over
-    const int sets = f8 && p.na * p.bn <= 128 ? (p.na * p.bn <= 64 ? 8 : 4) : 2;
+    // a set fills while another is read; e4m3 hands one over for each block, and
+    // more of them hide the hand-over
+    const int sets = p.na * p.bn <= 64 ? 8 : p.na * p.bn <= 128 ? 4 : 2;
     p.acc_log = sets == 8 ? 3 : sets == 4 ? 2 : 1;
     p.cols = sets * p.na * p.bn;
 
@@ -1140,14 +1154,14 @@ ep_status_t launch_on_device(const ep_buffer& b, LinearParams p, int64_t x_rows,
     if (!encode(&map_x, f8, p.x, 2, dx, sx, pair ? 128 : p.bn) || !encode(&map_w, f8, p.w, 4, dw, sw, 128))
         return fail(EP_ERR_UNSUPPORTED, "x or w is too large for a tensor map");
 
-    const auto kernel = pair ? (f8 ? linear_pair_kernel<true> : linear_pair_kernel<false>)
+    const auto kernel = pair ? (f8 ? linear_pair_kernel<true, true> : p.flush < p.kblocks ? linear_pair_kernel<false, true> : linear_pair_kernel<false, false>)
                         : f8 ? kernel_of<true>(split, p.bn) : kernel_of<false>(split, p.bn);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
     if (e != cudaSuccess) return fail(EP_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     const int64_t tiles = bound * p.nt, pairs = b.sm_count / 2, clusters = split ? clusters_of(b, p.splits) : 0;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(pair ? 2 * (tiles < pairs ? tiles : pairs) : split ? p.splits * (tiles < clusters ? tiles : clusters) : tiles < b.sm_count ? tiles : b.sm_count));
-    cfg.blockDim = dim3(pair ? kPairThreads : kThreads);
+    cfg.blockDim = dim3(pair ? kThreads : kThreads);
     cfg.dynamicSmemBytes = pair ? kPairSmem : smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
