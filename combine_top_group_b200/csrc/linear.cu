@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (c * 32 >= t.rows) continue;
                         uint32_t v[32];
                         tc::tmem_ld32(at + c * 32, v);
-                        tc::tmem_ld_wait();
+                        tc::tmem_ld_wait(v);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             ulonglong2 s2 = make_ulonglong2(one, one);
@@ -831,7 +831,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     for (int c = 0; c < 4; ++c) {
                         uint32_t v[32];
                         tc::tmem_ld32(at + column(c), v);
-                        tc::tmem_ld_wait();
+                        tc::tmem_ld_wait(v);
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
                             sum[SUM ? c * 16 + j : 0] = f32x2_fma_rn(
@@ -894,7 +894,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 } else {
                     uint32_t v[32];
                     tc::tmem_ld32(tmem + lane_base + (acc & 1) * 256 + column(c), v);
-                    tc::tmem_ld_wait();
+                    tc::tmem_ld_wait(v);
 #pragma unroll
                     for (int j = 0; j < 32; ++j) z[j] = __uint_as_float(v[j]);
                 }
