@@ -24,6 +24,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "ep.h"
@@ -82,7 +83,7 @@ __device__ __forceinline__ void group_rows(const LinearParams& p, int g, int64_t
 }
 
 __device__ __forceinline__ float activate(int act, float z) {
-    if (act == EP_ACT_SILU) return z / (1.0f + __expf(-z));
+    if (act == EP_ACT_SILU) return __fdividef(z, 1.0f + __expf(-z));
     if (act == EP_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
     return z;
 }
@@ -181,71 +182,115 @@ __device__ __forceinline__ void load_bias(const LinearParams& p, const Tile& t, 
         }
 }
 
-// One row of 128 channels, 4 to a lane: activation, residual, rounding, store.
-__device__ __forceinline__ void emit(const LinearParams& p, int64_t row, int n, float (&z)[4], const float (&u)[4]) {
-    const int lane = threadIdx.x & 31;
-    n += lane * 4;
-    if (p.act == EP_ACT_SWIGLU) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) z[i] = activate(EP_ACT_SILU, z[i]) * u[i];
-    } else if (p.act == EP_ACT_SILU) {
+__device__ __forceinline__ void activate4(int act, float (&z)[4]) {
+    if (act == EP_ACT_SILU) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) z[i] = activate(EP_ACT_SILU, z[i]);
-    } else if (p.act == EP_ACT_GELU) {
+    } else if (act == EP_ACT_GELU) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) z[i] = activate(EP_ACT_GELU, z[i]);
     }
-    const int64_t at = row * p.N + n;
-    if (p.vec) {
-        if (p.res && n < p.N) {
-            const uint2 r = *reinterpret_cast<const uint2*>(p.res + at);
-            z[0] += bf16lo(r.x);
-            z[1] += bf16hi(r.x);
-            z[2] += bf16lo(r.y);
-            z[3] += bf16hi(r.y);
-        }
-        if (p.out_type == EP_DTYPE_E4M3) {  // out_features is a multiple of 128: every lane holds channels
-            float amax = fmaxf(fmaxf(fabsf(z[0]), fabsf(z[1])), fmaxf(fabsf(z[2]), fabsf(z[3])));
-            amax = fmaxf(amax, 1e-4f);
+}
+
+// Four channels of a row, rounded and stored at `at`; e4m3: the warp holds a
+// block of 128, whose scale goes to *scale.
+template <int OUT>
+__device__ __forceinline__ void store4(const LinearParams& p, int64_t at, const float (&z)[4], float* scale) {
+    if (OUT == EP_DTYPE_E4M3) {
+        float amax = fmaxf(fmaxf(fabsf(z[0]), fabsf(z[1])), fmaxf(fabsf(z[2]), fabsf(z[3])));
+        amax = fmaxf(amax, 1e-4f);
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, o));
-            const float s = 448.0f / amax;
-            *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + at) =
-                pack_e4m3x2(z[0] * s, z[1] * s) | pack_e4m3x2(z[2] * s, z[3] * s) << 16;
-            if (lane == 0) p.out_scale[row * (p.N / 128) + n / 128] = amax / 448.0f;
-        } else if (n < p.N) {
-            if (p.out_type == EP_DTYPE_FP32)
-                *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(z[0], z[1], z[2], z[3]);
-            else
-                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
-                    make_uint2(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]));
-        }
-        return;
+        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, o));
+        const float s = 448.0f / amax;
+        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + at) =
+            pack_e4m3x2(z[0] * s, z[1] * s) | pack_e4m3x2(z[2] * s, z[3] * s) << 16;
+        if ((threadIdx.x & 31) == 0) *scale = amax / 448.0f;
+    } else if (OUT == EP_DTYPE_FP32) {
+        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(z[0], z[1], z[2], z[3]);
+    } else {
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
+            make_uint2(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]));
     }
+}
+__device__ __forceinline__ void add_residual(const LinearParams& p, int64_t at, float (&z)[4]) {
+    const uint2 r = *reinterpret_cast<const uint2*>(p.res + at);
+    z[0] += bf16lo(r.x);
+    z[1] += bf16hi(r.x);
+    z[2] += bf16lo(r.y);
+    z[3] += bf16hi(r.y);
+}
+
+// Staged rows i = first, first + kEpiWarps, ... < own, which are rows
+// row + (i - first) * gap of the output, 4 channels of each tile to a lane:
+// gate and up of 128 channels, or one or two neighbouring tiles. load(i, s)
+// gives the lane's 4 sums of row i, tile s. What is the same for all rows is
+// settled outside the loop (choosing per row took half of the epilogue). VEC:
+// rows of out and residual allow 4-channel accesses (out_features % 4 == 0).
+template <int OUT, bool GATED, bool VEC, typename Load>
+__device__ __forceinline__ void emit_rows(const LinearParams& p, const Tile& t, int subs, const Bias& b, int first, int own,
+                                          int64_t row, int gap, Load load) {
+    const int lane4 = (threadIdx.x & 31) * 4;
+    const int n0 = channel_of(p, t, 0) + lane4, n1 = channel_of(p, t, 1) + lane4;
+    const bool two = !GATED && subs == 2, on0 = n0 < p.N, on1 = two && n1 < p.N;
+    int64_t at = row * p.N;
+    const int64_t stride = (int64_t)gap * kEpiWarps * p.N;
+    const int blocks = p.N / 128;
+    float* scale = OUT == EP_DTYPE_E4M3 ? p.out_scale + row * blocks + channel_of(p, t, 0) / 128 : nullptr;
+#pragma unroll 1
+    for (int i = first; i < own; i += kEpiWarps, at += stride) {
+        const float4 v = load(i, 0), w = GATED || two ? load(i, 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+        float z[4] = {v.x + b.v[0][0], v.y + b.v[0][1], v.z + b.v[0][2], v.w + b.v[0][3]};
+        float u[4] = {w.x + b.v[1][0], w.y + b.v[1][1], w.z + b.v[1][2], w.w + b.v[1][3]};
+        if (GATED) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (n + i >= p.N) continue;
-        if (p.res) z[i] += __uint_as_float((uint32_t)p.res[at + i] << 16);
-        if (p.out_type == EP_DTYPE_FP32) static_cast<float*>(p.out)[at + i] = z[i];
-        else static_cast<uint16_t*>(p.out)[at + i] = (uint16_t)(pack_bf16x2(z[i], 0.f) & 0xffff);
+            for (int k = 0; k < 4; ++k) z[k] = activate(EP_ACT_SILU, z[k]) * u[k];
+        } else {
+            activate4(p.act, z);
+            if (two) activate4(p.act, u);
+        }
+        if (VEC) {
+            if (p.res) {
+                if (on0) add_residual(p, at + n0, z);
+                if (on1) add_residual(p, at + n1, u);
+            }
+            // e4m3: out_features is a multiple of 128, so on0 and on1 hold for whole warps
+            if (on0) store4<OUT>(p, at + n0, z, scale);
+            if (on1) store4<OUT>(p, at + n1, u, scale + 1);
+            if (OUT == EP_DTYPE_E4M3) scale += (int64_t)gap * kEpiWarps * blocks;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const int n = (s ? n1 : n0) + k;
+                    if (n >= p.N || (s && !two)) continue;
+                    float y = s ? u[k] : z[k];
+                    if (p.res) y += __uint_as_float((uint32_t)p.res[at + n] << 16);
+                    if (OUT == EP_DTYPE_FP32) static_cast<float*>(p.out)[at + n] = y;
+                    else static_cast<uint16_t*>(p.out)[at + n] = (uint16_t)(pack_bf16x2(y, 0.f) & 0xffff);
+                }
+            }
+        }
     }
 }
 
-// A staged row: gate and up 128 channels each, or two neighbouring tiles.
 template <typename Load>
-__device__ __forceinline__ void emit_row(const LinearParams& p, const Tile& t, int subs, const Bias& b, int64_t row,
-                                         Load load) {
-    float z[2][4];
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        const float4 v = s < subs ? load(s) : make_float4(0.f, 0.f, 0.f, 0.f);
-        z[s][0] = v.x + b.v[s][0];
-        z[s][1] = v.y + b.v[s][1];
-        z[s][2] = v.z + b.v[s][2];
-        z[s][3] = v.w + b.v[s][3];
-    }
-    emit(p, row, channel_of(p, t, 0), z[0], z[1]);
-    if (p.parts == 1 && subs == 2) emit(p, row, channel_of(p, t, 1), z[1], z[0]);
+__device__ __forceinline__ void emit_chunk(const LinearParams& p, const Tile& t, int subs, const Bias& b, int first, int own,
+                                           int64_t row, int gap, Load load) {
+    const bool gated = p.parts == 2;
+    auto as = [&](auto out) {
+        constexpr int OUT = decltype(out)::value;
+        if (OUT == EP_DTYPE_E4M3 || p.vec) {
+            if (gated) emit_rows<OUT, true, true>(p, t, subs, b, first, own, row, gap, load);
+            else emit_rows<OUT, false, true>(p, t, subs, b, first, own, row, gap, load);
+        } else {
+            if (gated) emit_rows<OUT, true, false>(p, t, subs, b, first, own, row, gap, load);
+            else emit_rows<OUT, false, false>(p, t, subs, b, first, own, row, gap, load);
+        }
+    };
+    if (p.out_type == EP_DTYPE_BF16) as(std::integral_constant<int, EP_DTYPE_BF16>());
+    else if (p.out_type == EP_DTYPE_FP32) as(std::integral_constant<int, EP_DTYPE_FP32>());
+    else as(std::integral_constant<int, EP_DTYPE_E4M3>());
 }
 
 // Barrier of the epilogue warps; the _and form tells whether all of them are ok.
@@ -510,70 +555,69 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int width = subs * 128;
             // all warps leave after the same tile: none may wait below for one that left
             ok = epi_sync_and(ok);
-#pragma unroll
-            for (int c = 0; c < BN / 32; ++c) {
-                if (c * 32 >= t.rows) continue;
-                uint32_t v[32];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float2 f = f32x2_unpack(sum[c * 16 + j]);
-                    v[2 * j] = __float_as_uint(f.x);
-                    v[2 * j + 1] = __float_as_uint(f.y);
-                }
+            // the rows of a chunk that are this CTA's: rank, rank + splits, ...
+            const int slots = (32 + p.splits - 1) / p.splits;  // of a CTA, at most
+#pragma unroll 1
+            for (int c = 0; c * 32 < t.rows; ++c) {
+                const int rows = min(32, t.rows - c * 32), b = use & 1;
+                const int own = SPLIT ? (rows + p.splits - 1 - rank) / p.splits : rows;  // this CTA's
+                const float* box = staging + (SPLIT ? b * (kInbox / 8) : 0);
                 if (SPLIT) {
                     // Row r of the chunk belongs to CTA r % splits. All CTAs push
                     // their sums of it into that one's inbox, which adds them in
                     // the order of the CTAs. Two inboxes alternate.
-                    const int b = use & 1, rows = min(32, t.rows - c * 32);
-                    const int slots = (32 + p.splits - 1) / p.splits;  // rows of a CTA, at most
                     if (use >= 2) ok = tc::bar_wait(inbox_free(b), (use / 2 - 1) & 1, stop) && ok;
                     if (threadIdx.x == 0)
-                        tc::bar_expect(inbox_full(b), (rows + p.splits - 1 - rank) / p.splits * p.splits * width * 4);
-                    if (ok && sub < subs) {
-                        const uint32_t to =
-                            tc::smem_u32(staging) + b * (kInbox / 2) + (rank * slots * width + col) * 4;
-                        int owner = 0, slot = 0;
+                        tc::bar_expect(inbox_full(b), own * p.splits * width * 4);
+                } else if (c > 0) {
+                    epi_sync();  // staging is free
+                }
+                if (ok && sub < subs) {
+                    const uint32_t to = tc::smem_u32(box) + ((SPLIT ? rank * slots * width : 0) + col) * 4;
+                    int owner = 0;
+                    uint32_t at = to;
+#pragma unroll
+                    for (int q = 0; q < BN / 32; ++q) {
+                        if (c != q) continue;
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
+                            const float2 f = f32x2_unpack(sum[q * 16 + j / 2]);
+                            const float v = j & 1 ? f.y : f.x;
+                            if (!SPLIT) {
+                                staging[j * width + col] = v;
+                                continue;
+                            }
                             if (j < rows)
-                                tc::push(tc::peer_smem(to + slot * width * 4, owner), v[j],
-                                         tc::peer_smem(inbox_full(b), owner));
+                                tc::push(tc::peer_smem(at, owner), __float_as_uint(v), tc::peer_smem(inbox_full(b), owner));
                             if (++owner == p.splits) {
                                 owner = 0;
-                                ++slot;
+                                at += width * 4;
                             }
                         }
                     }
+                }
+                if (SPLIT) {
                     ok = tc::bar_wait(inbox_full(b), (use / 2) & 1, stop) && ok;
                     ok = epi_sync_and(ok);
-                    const float* box = staging + b * (kInbox / 8);
-                    if (ok)
-                        for (int i = warp; rank + i * p.splits < rows; i += kEpiWarps)
-                            emit_row(p, t, subs, bias, t.row + c * 32 + rank + i * p.splits, [&](int s) {
-                                const float* from = box + i * width + s * 128 + lane * 4;
-                                float4 a = *reinterpret_cast<const float4*>(from);
-                                for (int q = 1; q < p.splits; ++q) {
-                                    const float4 w = *reinterpret_cast<const float4*>(from + q * slots * width);
-                                    a = make_float4(a.x + w.x, a.y + w.y, a.z + w.z, a.w + w.w);
-                                }
-                                return a;
-                            });
+                } else {
+                    epi_sync();
+                }
+                if (ok)
+                    emit_chunk(p, t, subs, bias, warp, own, t.row + c * 32 + (SPLIT ? rank + warp * p.splits : warp),
+                               SPLIT ? p.splits : 1, [&](int i, int s) {
+                                   const float* from = box + i * width + s * 128 + lane * 4;
+                                   float4 a = *reinterpret_cast<const float4*>(from);
+                                   if (SPLIT)
+                                       for (int q = 1; q < p.splits; ++q) {
+                                           const float4 w = *reinterpret_cast<const float4*>(from + q * slots * width);
+                                           a = make_float4(a.x + w.x, a.y + w.y, a.z + w.z, a.w + w.w);
+                                       }
+                                   return a;
+                               });
+                if (SPLIT) {
                     epi_sync();
                     if (threadIdx.x < p.splits) tc::bar_arrive_at(tc::peer_smem(inbox_free(b), threadIdx.x));
                     ++use;
-                } else {
-                    if (c > 0) epi_sync();  // staging is free
-                    float* row0 = staging + col;
-                    if (ok && sub < subs) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) row0[j * width] = __uint_as_float(v[j]);
-                    }
-                    epi_sync();
-                    if (ok)
-                        for (int r = warp; r < 32 && c * 32 + r < t.rows; r += kEpiWarps)
-                            emit_row(p, t, subs, bias, t.row + c * 32 + r, [&](int s) {
-                                return *reinterpret_cast<const float4*>(staging + r * width + s * 128 + lane * 4);
-                            });
                 }
             }
         }
@@ -1088,7 +1132,7 @@ Shape shape_of(const ep_buffer& b, const LinearParams& p, int64_t avg, int64_t m
     }
     // A cluster can share each tile's in_features: n CTAs finish a tile n times
     // as fast, less the exchange of its sums, and rounds over all tiles come
-    // out less ragged. The exchange takes 2 us.
+    // out less ragged. The exchange takes 1.5 us for each 32 rows.
     c.splits = 1;
     const double block = c.bn < 128 ? (f8 ? 0.45 : 0.28) : (f8 ? 0.67 : 0.25) * c.na;
     double best = 0;
@@ -1096,7 +1140,7 @@ Shape shape_of(const ep_buffer& b, const LinearParams& p, int64_t avg, int64_t m
         const int64_t at_once = n == 1 ? b.sm_count : clusters_of(b, n);
         if (at_once < 1) continue;
         const int64_t rounds = (likely * c.nt + at_once - 1) / at_once;
-        const double time = rounds * ((p.kblocks + n - 1) / n * block + (n > 1 ? 2.0 : 0.5));
+        const double time = rounds * ((p.kblocks + n - 1) / n * block + (n > 1 ? 1.5 * (c.bn / 32) : 0.5));
         if (n == 1 || time < best) {
             best = time;
             c.splits = n;
@@ -1105,7 +1149,7 @@ Shape shape_of(const ep_buffer& b, const LinearParams& p, int64_t avg, int64_t m
     if (avg < 256 || p.wide < 256) return c;
     double rounds_p = (p.G == 1 ? (double)tiles(256) : groups * (avg / 256.0 + 0.5)) * ((p.wide + 255) / 256) / (b.sm_count / 2);
     if (rounds_p < 4) rounds_p = ceil(rounds_p);
-    const double time_p = rounds_p * p.kblocks * (f8 ? 0.88 : 0.28);
+    const double time_p = rounds_p * p.kblocks * (f8 ? 0.88 : 0.28) + 2.0;
     if (time_p > best) return c;
     c.pair = true;
     c.bn = 256;
