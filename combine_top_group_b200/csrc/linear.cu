@@ -645,78 +645,88 @@ constexpr int kPairEpiRegs = 224, kPairOtherRegs = 56;  // as kEpiRegs and kOthe
 static_assert(2 * 128 * kPairEpiRegs + 128 * kPairOtherRegs == kThreads * 168, "register split");
 constexpr int kPairStage = 2 * kSub;
 constexpr int kPairStages = 6;
-constexpr int kPairSmem = kPairStages * kPairStage + 256 + 2 * 128 * 4 + 1024;
+constexpr int kPairSmem = kPairStages * kPairStage + kEpiWarps * 4096 + 256 + 2 * 128 * 4 + 1024;
+static_assert(kPairSmem <= kSmemMax, "shared memory");
 
-// 32 channels from n of a row, rounded and stored.
-__device__ __forceinline__ void store32(const LinearParams& p, int64_t row, int n, const float (&y)[32], float scale) {
-    const int64_t at = row * p.N + n;
-    if (p.out_type == EP_DTYPE_E4M3) {
-        uint4* o = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + at);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float* v = y + 16 * i + 4 * j;
-                w[j] = pack_e4m3x2(v[0] * scale, v[1] * scale) | pack_e4m3x2(v[2] * scale, v[3] * scale) << 16;
-            }
-            o[i] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        return;
-    }
-    if (p.out_type == EP_DTYPE_FP32) {
-        float* o = static_cast<float*>(p.out) + at;
-#pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-            if (p.N % 4 == 0) {
-                if (n + i < p.N) *reinterpret_cast<float4*>(o + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (n + i + j < p.N) o[i + j] = y[i + j];
-            }
-        }
-        return;
-    }
-    uint16_t* o = static_cast<uint16_t*>(p.out) + at;
-#pragma unroll
-    for (int i = 0; i < 32; i += 8) {
+// A warp's outputs go through 4 KB of shared memory: each lane puts 16-byte
+// pieces of its row there (32 rows of 128 bytes), and the warp stores whole
+// rows' pieces together. Lanes that store their own rows touch 32 lines with
+// each instruction, which took 2.5 to 6.6 us for a tile.
+// Pieces of a row are swapped by row & 7, so that neither side meets in banks.
+__device__ __forceinline__ void stage_pieces(uint4* box, int r, int at, int out_type, const float (&y)[16], float scale) {
+    uint4* row = box + r * 8;
+    const int x = r & 7;
+    if (out_type == EP_DTYPE_E4M3) {
         uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(y[i + 2 * j], y[i + 2 * j + 1]);
-        if (p.N % 8 == 0) {
-            if (n + i < p.N) *reinterpret_cast<uint4*>(o + i) = make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
+        for (int j = 0; j < 4; ++j)
+            w[j] = pack_e4m3x2(y[4 * j] * scale, y[4 * j + 1] * scale) |
+                   pack_e4m3x2(y[4 * j + 2] * scale, y[4 * j + 3] * scale) << 16;
+        row[at ^ x] = make_uint4(w[0], w[1], w[2], w[3]);
+    } else if (out_type == EP_DTYPE_FP32) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (n + i + j < p.N) o[i + j] = (uint16_t)(w[j / 2] >> 16 * (j & 1));
-        }
+        for (int i = 0; i < 4; ++i)
+            row[(at + i) ^ x] = make_uint4(__float_as_uint(y[4 * i]), __float_as_uint(y[4 * i + 1]),
+                                           __float_as_uint(y[4 * i + 2]), __float_as_uint(y[4 * i + 3]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            row[(at + i) ^ x] = make_uint4(pack_bf16x2(y[8 * i], y[8 * i + 1]), pack_bf16x2(y[8 * i + 2], y[8 * i + 3]),
+                                           pack_bf16x2(y[8 * i + 4], y[8 * i + 5]), pack_bf16x2(y[8 * i + 6], y[8 * i + 7]));
+    }
+}
+// Stores `pieces` of each of the warp's first `rows` rows, channels from n;
+// rows start at `row`. size: bytes of a channel; size * out_features is a multiple of 16.
+__device__ __forceinline__ void flush_pieces(const LinearParams& p, const uint4* box, int pieces, int rows, int64_t row,
+                                             int n, int size) {
+    const int lane = threadIdx.x & 31, piece = lane & 7;
+    __syncwarp();
+    const bool on = piece < pieces && n + piece * (16 / size) < p.N;
+    uint8_t* out = static_cast<uint8_t*>(p.out) + ((row + lane / 8) * p.N + n) * size + piece * 16;
+    const int64_t step = (int64_t)4 * p.N * size;
+#pragma unroll 2
+    for (int i = 0; i < 8; ++i) {
+        const int r = i * 4 + lane / 8;
+        if (on && r < rows) *reinterpret_cast<uint4*>(out + i * step) = box[r * 8 + (piece ^ (r & 7))];
+    }
+    __syncwarp();
+}
+// The same values one by one, for rows that are no multiple of 16 bytes.
+__device__ __forceinline__ void store_scalars(const LinearParams& p, int64_t row, int n, const float (&y)[16]) {
+    const int64_t at = row * p.N + n;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        if (n + i >= p.N) continue;
+        if (p.out_type == EP_DTYPE_FP32) static_cast<float*>(p.out)[at + i] = y[i];
+        else static_cast<uint16_t*>(p.out)[at + i] = (uint16_t)(pack_bf16x2(y[i], 0.f) & 0xffff);
     }
 }
 
-// Bias, activation and residual of 32 channels from n of a row.
-__device__ __forceinline__ void finish32(const LinearParams& p, int g, int64_t row, int n, const float (&z)[32],
-                                         const float (&u)[32], float (&y)[32]) {
+// Bias, activation and residual of 16 channels from n of a row: y, with u its
+// other half where gated. One choice of the activation for all channels: a
+// branch for each cost more than the products of a 2048-channel layer (503
+// against 1260 TFLOP/s).
+__device__ __forceinline__ void finish16(const LinearParams& p, int g, int64_t row, int n, float (&y)[16], const float (&u)[16]) {
     const float* bias = p.bias ? p.bias + (int64_t)g * p.wide + n : nullptr;
+    if (bias) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) y[i] = z[i] + (bias && n + i < p.N ? bias[i] : 0.f);
-    // one choice for all channels: a branch for each cost more than the products
-    // of a 2048-channel layer (503 against 1260 TFLOP/s)
+        for (int i = 0; i < 16; ++i) y[i] += n + i < p.N ? bias[i] : 0.f;
+    }
     if (p.act == EP_ACT_SWIGLU) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
+        for (int i = 0; i < 16; ++i)
             y[i] = activate(EP_ACT_SILU, y[i]) * (u[i] + (bias && n + i < p.N ? bias[p.N + i] : 0.f));
     } else if (p.act == EP_ACT_SILU) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) y[i] = activate(EP_ACT_SILU, y[i]);
+        for (int i = 0; i < 16; ++i) y[i] = activate(EP_ACT_SILU, y[i]);
     } else if (p.act == EP_ACT_GELU) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) y[i] = activate(EP_ACT_GELU, y[i]);
+        for (int i = 0; i < 16; ++i) y[i] = activate(EP_ACT_GELU, y[i]);
     }
     if (p.res) {
         const uint16_t* r = p.res + row * p.N + n;
 #pragma unroll
-        for (int i = 0; i < 32; i += 8) {
+        for (int i = 0; i < 16; i += 8) {
             if (p.N % 8 == 0) {
                 if (n + i >= p.N) continue;
                 const uint4 v = *reinterpret_cast<const uint4*>(r + i);
@@ -743,7 +753,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                        LinearParams p) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t ring = (tc::smem_u32(smem_raw) + 1023) & ~1023u;
-    uint8_t* control = smem_raw + (ring - tc::smem_u32(smem_raw)) + kPairStages * kPairStage;
+    uint8_t* boxes = smem_raw + (ring - tc::smem_u32(smem_raw)) + kPairStages * kPairStage;
+    uint8_t* control = boxes + kEpiWarps * 4096;
     float* row_amax = reinterpret_cast<float*>(control + 256);  // [2][128]
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(control + 240);
     volatile uint32_t* stop = reinterpret_cast<uint32_t*>(control + 244);
@@ -927,23 +938,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             // all warps leave after the same tile: none may wait below for one that left
             ok = epi_sync_and(ok);
-            auto load = [&](int c, float(&z)[32]) {
+            auto load = [&](int c, float(&z)[16]) {  // 16 channels
                 if (SUM) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float2 v = f32x2_unpack(sum[SUM ? c * 16 + j : 0]);
+                    for (int j = 0; j < 8; ++j) {
+                        const float2 v = f32x2_unpack(sum[SUM ? c * 8 + j : 0]);
                         z[2 * j] = v.x;
                         z[2 * j + 1] = v.y;
                     }
                 } else {
-                    uint32_t v[32];
-                    tc::tmem_ld32(tmem + lane_base + (acc & 1) * 256 + column(c), v);
-                    tc::tmem_ld_wait(v);
+                    uint32_t v[16];
+                    tc::tmem_read16(tmem + lane_base + (acc & 1) * 256 + column(c >> 1) + (c & 1) * 16, v);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) z[j] = __uint_as_float(v[j]);
+                    for (int j = 0; j < 16; ++j) z[j] = __uint_as_float(v[j]);
                 }
             };
             const bool e4m3 = p.out_type == EP_DTYPE_E4M3;
+            const int size = e4m3 ? 1 : p.out_type == EP_DTYPE_FP32 ? 4 : 2;  // bytes of a channel
+            const bool whole = p.N * size % 16 == 0;
+            uint4* box = reinterpret_cast<uint4*>(boxes + warp * 4096);
             float amax = 1e-4f;
             if (ok && rows > (warp & 3) * 32) {
                 // e4m3 goes over the row twice: for its amax, then to store it
@@ -958,18 +971,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         p.out_scale[row * (p.N / 128) + n0 / 128] = amax / 448.0f;
                     const float scale = 448.0f / amax;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        if (c >= (gated ? 2 : 4) || n0 + c * 32 >= p.N) continue;
-                        float z[32], u[32], y[32];
-                        load(c, z);
-                        if (gated) load((c + 2) & 3, u);
-                        if (!live) continue;
-                        finish32(p, g, row, n0 + c * 32, z, u, y);
+                    for (int c = 0; c < 8; ++c) {
+                        if (c >= (gated ? 4 : 8) || n0 + c * 16 >= p.N) continue;
+                        float y[16], u[16];
+                        load(c, y);
+                        if (gated) load((c + 4) & 7, u);
+                        if (live) finish16(p, g, row, n0 + c * 16, y, u);
                         if (pass == 0) {
+                            if (live) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(y[i]));
-                        } else {
-                            store32(p, row, n0 + c * 32, y, scale);
+                                for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(y[i]));
+                            }
+                        } else if (whole) {
+                            const int at = c * size & 7;  // first piece of the chunk
+                            if (live) stage_pieces(box, lane, at, p.out_type, y, scale);
+                            if (at + size == 8 || c == (gated ? 3 : 7) || n0 + c * 16 + 16 >= p.N)
+                                flush_pieces(p, box, at + size, rows - (warp & 3) * 32,
+                                             t.row + rank * 128 + (warp & 3) * 32, n0 + c * 16 - at * 16 / size, size);
+                        } else if (live) {
+                            store_scalars(p, row, n0 + c * 16, y);
                         }
                     }
                 }
@@ -1109,20 +1129,28 @@ struct Shape {
     int64_t bound;  // row tiles there can be
 };
 
-// Takes the kernel with the least time by this estimate, in microseconds for
-// 128 bytes of in_features, as measured on large layers: 0.28 (bf16) or 0.88
-// (e4m3) for a pair's 256 x 256 tile; 0.50 or 1.34 for a CTA's 128 rows x 256
-// channels, half of that with 128 channels, and 0.28 or 0.45 where its rows are
-// few (it then waits for weights). With pairs an expert's last tile is half
-// empty in the mean.
+// Takes the kernel with the least time by this estimate, in microseconds as
+// measured on large layers. A 128-byte block of in_features takes 0.28 (bf16)
+// or 0.66 (e4m3) for a pair's 256 x 256 tile; 0.25 or 0.51 for 128 rows and
+// each weight tile of a CTA, 0.28 or 0.45 where its rows are few (it then waits
+// for weights). A tile's epilogue takes 4.5 with pairs, else 0.7 for each 32 rows
+// and weight tile; with bf16 it runs beside the next tile's products. Among
+// groups, the last of a group's tiles is half empty in the mean.
 Shape shape_of(const ep_buffer& b, const LinearParams& p, int64_t avg, int64_t most) {
     const bool f8 = p.x_scale != nullptr;
     const int64_t groups = most < p.G ? most : p.G;
-    auto tiles = [&](int rows) { return p.G == 1 ? (avg + rows - 1) / rows : groups * ((avg + rows - 1) / rows); };
+    auto row_tiles = [&](int rows) {
+        if (p.G == 1) return (double)((avg + rows - 1) / rows);
+        return groups * fmax(1.0, (double)avg / rows + 0.5);
+    };
+    auto total = [&](double tiles, int64_t at_once, double products, double epilogue) {
+        const double rounds = fmax(1.0, tiles / at_once < 4 ? ceil(tiles / at_once) : tiles / at_once);
+        return f8 ? rounds * (products + epilogue) : rounds * fmax(products, epilogue) + epilogue;
+    };
     Shape c{};
     c.bn = avg <= 32 ? 32 : avg <= 64 ? 64 : 128;
     c.bound = p.cnt ? (int64_t)p.G * ((p.region + c.bn - 1) / c.bn) : most / c.bn + groups;
-    const int64_t likely = tiles(c.bn);
+    const double likely = row_tiles(c.bn);
     // two weight tiles per CTA share its rows of x; one where tiles are few
     c.na = 2;
     c.nt = p.parts == 2 ? (p.N + 127) / 128 : (p.N + 255) / 256;
@@ -1131,31 +1159,28 @@ Shape shape_of(const ep_buffer& b, const LinearParams& p, int64_t avg, int64_t m
         c.nt = (p.N + 127) / 128;
     }
     // A cluster can share each tile's in_features: n CTAs finish a tile n times
-    // as fast, less the exchange of its sums, and rounds over all tiles come
-    // out less ragged. The exchange takes 1.5 us for each 32 rows.
-    c.splits = 1;
-    const double block = c.bn < 128 ? (f8 ? 0.45 : 0.28) : (f8 ? 0.67 : 0.25) * c.na;
+    // as fast, less the exchange of its sums (1.5 for each 32 rows), and rounds
+    // over all tiles come out less ragged.
+    const double block = c.bn < 128 ? (f8 ? 0.45 : 0.28) : (f8 ? 0.51 : 0.25) * c.na, epilogue = c.bn / 32 * c.na * 0.7;
     double best = 0;
-    for (int n = 1; n <= kMaxSplits && p.kblocks >= 4 * n; ++n) {
+    c.splits = 1;
+    for (int n = 1; n <= kMaxSplits && (n == 1 || p.kblocks >= 4 * n); ++n) {
         const int64_t at_once = n == 1 ? b.sm_count : clusters_of(b, n);
         if (at_once < 1) continue;
-        const int64_t rounds = (likely * c.nt + at_once - 1) / at_once;
-        const double time = rounds * ((p.kblocks + n - 1) / n * block + (n > 1 ? 1.5 * (c.bn / 32) : 0.5));
+        const double time = total(likely * c.nt, at_once, (p.kblocks + n - 1) / n * block, epilogue + (n > 1 ? 1.5 * (c.bn / 32) : 0));
         if (n == 1 || time < best) {
             best = time;
             c.splits = n;
         }
     }
-    if (avg < 256 || p.wide < 256) return c;
-    double rounds_p = (p.G == 1 ? (double)tiles(256) : groups * (avg / 256.0 + 0.5)) * ((p.wide + 255) / 256) / (b.sm_count / 2);
-    if (rounds_p < 4) rounds_p = ceil(rounds_p);
-    const double time_p = rounds_p * p.kblocks * (f8 ? 0.88 : 0.28) + 2.0;
-    if (time_p > best) return c;
+    if (avg < 128 || p.wide < 256) return c;
+    const int nt = p.parts == 2 ? (p.N + 127) / 128 : (p.N + 255) / 256;
+    if (total(row_tiles(256) * nt, b.sm_count / 2, p.kblocks * (f8 ? 0.66 : 0.28), 4.5) > best) return c;
     c.pair = true;
     c.bn = 256;
     c.na = 2;
     c.splits = 1;
-    c.nt = p.parts == 2 ? (p.N + 127) / 128 : (p.N + 255) / 256;
+    c.nt = nt;
     c.bound = p.cnt ? (int64_t)p.G * ((p.region + 255) / 256) : most / 256 + groups;
     return c;
 }
