@@ -1131,9 +1131,9 @@ struct Shape {
 
 // Takes the kernel with the least time by this estimate, in microseconds as
 // measured on large layers. A 128-byte block of in_features takes 0.28 (bf16)
-// or 0.66 (e4m3) for a pair's 256 x 256 tile; 0.25 or 0.51 for 128 rows and
-// each weight tile of a CTA, 0.28 or 0.45 where its rows are few (it then waits
-// for weights). A tile's epilogue takes 4.5 with pairs, else 0.7 for each 32 rows
+// or 0.62 (e4m3) for a pair's 256 x 256 tile; 0.25 or 0.51 for 128 rows and
+// each weight tile of a CTA; 0.16 + 0.10 or 0.25 + 0.12 for each of them where
+// its rows are few (it then waits for weights). A tile's epilogue takes 4.5 or 11 with pairs, else 0.7 for each 32 rows
 // and weight tile; with bf16 it runs beside the next tile's products. Among
 // groups, the last of a group's tiles is half empty in the mean.
 Shape shape_of(const ep_buffer& b, const LinearParams& p, int64_t avg, int64_t most) {
@@ -1145,37 +1145,40 @@ Shape shape_of(const ep_buffer& b, const LinearParams& p, int64_t avg, int64_t m
     };
     auto total = [&](double tiles, int64_t at_once, double products, double epilogue) {
         const double rounds = fmax(1.0, tiles / at_once < 4 ? ceil(tiles / at_once) : tiles / at_once);
-        return f8 ? rounds * (products + epilogue) : rounds * fmax(products, epilogue) + epilogue;
+        return f8 ? rounds * (products + epilogue) : (rounds - 1) * fmax(products, epilogue) + products + epilogue;
     };
     Shape c{};
-    c.bn = avg <= 32 ? 32 : avg <= 64 ? 64 : 128;
-    c.bound = p.cnt ? (int64_t)p.G * ((p.region + c.bn - 1) / c.bn) : most / c.bn + groups;
-    const double likely = row_tiles(c.bn);
-    // two weight tiles per CTA share its rows of x; one where tiles are few
-    c.na = 2;
-    c.nt = p.parts == 2 ? (p.N + 127) / 128 : (p.N + 255) / 256;
-    if (p.parts == 1 && (p.N <= 128 || likely * c.nt < b.sm_count)) {
-        c.na = 1;
-        c.nt = (p.N + 127) / 128;
-    }
-    // A cluster can share each tile's in_features: n CTAs finish a tile n times
-    // as fast, less the exchange of its sums (1.5 for each 32 rows), and rounds
-    // over all tiles come out less ragged.
-    const double block = c.bn < 128 ? (f8 ? 0.45 : 0.28) : (f8 ? 0.51 : 0.25) * c.na, epilogue = c.bn / 32 * c.na * 0.7;
     double best = 0;
-    c.splits = 1;
-    for (int n = 1; n <= kMaxSplits && (n == 1 || p.kblocks >= 4 * n); ++n) {
-        const int64_t at_once = n == 1 ? b.sm_count : clusters_of(b, n);
-        if (at_once < 1) continue;
-        const double time = total(likely * c.nt, at_once, (p.kblocks + n - 1) / n * block, epilogue + (n > 1 ? 1.5 * (c.bn / 32) : 0));
-        if (n == 1 || time < best) {
+    for (int bn = avg <= 32 ? 32 : avg <= 64 ? 64 : 128; bn >= 32; bn /= 2) {
+        const double likely = row_tiles(bn);
+        // two weight tiles per CTA share its rows of x; one where tiles are few
+        int na = 2, nt = p.parts == 2 ? (p.N + 127) / 128 : (p.N + 255) / 256;
+        if (p.parts == 1 && (p.N <= 128 || likely * nt < b.sm_count)) {
+            na = 1;
+            nt = (p.N + 127) / 128;
+        }
+        const double block = bn == 128 ? (f8 ? 0.51 : 0.25) * na : (f8 ? 0.25 : 0.16) + (f8 ? 0.12 : 0.10) * na;
+        const double epilogue = bn / 32 * na * 0.7;
+        // A cluster can share each tile's in_features: n CTAs finish a tile n
+        // times as fast, less the exchange of its sums (1.5 for each 32 rows),
+        // and rounds over all tiles come out less ragged.
+        for (int n = 1; n <= kMaxSplits && (n == 1 || p.kblocks >= 4 * n); ++n) {
+            const int64_t at_once = n == 1 ? b.sm_count : clusters_of(b, n);
+            if (at_once < 1) continue;
+            const double time =
+                total(likely * nt, at_once, (p.kblocks + n - 1) / n * block, epilogue + (n > 1 ? 1.5 * (bn / 32) : 0));
+            if (c.splits > 0 && time >= best) continue;
             best = time;
+            c.bn = bn;
+            c.na = na;
+            c.nt = nt;
             c.splits = n;
         }
     }
+    c.bound = p.cnt ? (int64_t)p.G * ((p.region + c.bn - 1) / c.bn) : most / c.bn + groups;
     if (avg < 128 || p.wide < 256) return c;
     const int nt = p.parts == 2 ? (p.N + 127) / 128 : (p.N + 255) / 256;
-    if (total(row_tiles(256) * nt, b.sm_count / 2, p.kblocks * (f8 ? 0.66 : 0.28), 4.5) > best) return c;
+    if (total(row_tiles(256) * nt, b.sm_count / 2, p.kblocks * (f8 ? 0.62 : 0.28), f8 ? 11.0 : 4.5) > best) return c;
     c.pair = true;
     c.bn = 256;
     c.na = 2;

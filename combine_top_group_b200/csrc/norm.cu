@@ -614,16 +614,38 @@ int64_t bwd_slots(int64_t N, int tpr) {
     return rows < most ? rows : most;
 }
 
-// CTAs that the device holds at once (per SM, on its SMs); 0 on an error.
+constexpr int kMaxStreamSmem = 226 * 1024;  // beside the reduction's static 256 bytes
+
+// CTAs that the current device holds at once (per SM, on its SMs); 0 on an
+// error. Sets the kernel's shared-memory limit. The host thread's last counts
+// are kept, since asking takes longer than the launch; the limit is set by every
+// call, always to the same value: a reset of the device forgets it.
 int resident(const void* kernel, int threads, int smem, int* per, int* sms) {
+    struct Known {
+        const void* kernel;
+        int threads, smem, dev, per, sms;
+    };
+    static thread_local Known known{};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(per, kernel, threads, smem) != cudaSuccess) {
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxStreamSmem) != cudaSuccess) {
         cudaGetLastError();
         return 0;
     }
+    if (known.kernel != kernel || known.threads != threads || known.smem != smem || known.dev != dev) {
+        known.kernel = nullptr;
+        if (cudaDeviceGetAttribute(&known.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&known.per, kernel, threads, smem) != cudaSuccess) {
+            cudaGetLastError();
+            return 0;
+        }
+        known.kernel = kernel;
+        known.threads = threads;
+        known.smem = smem;
+        known.dev = dev;
+    }
+    *per = known.per;
+    *sms = known.sms;
     return *per * *sms;
 }
 

@@ -458,7 +458,7 @@ def _why_not(t, dtypes, dev: int, shape) -> str:
         return "is no tensor"
     if t.dtype not in dtypes:
         return f"has dtype {t.dtype}, not {' or '.join(str(d) for d in dtypes)}"
-    if t.get_device() != dev or not t.is_cuda:
+    if t.get_device() != dev or dev < 0:
         return f"is on {t.device}, not on the CUDA device of the call"
     if not t.is_contiguous():
         return "is not contiguous"
@@ -469,8 +469,9 @@ def _checked(where: str, dev: int, *wanted) -> None:
     """Each of `wanted` is (name, tensor or None, dtypes, shape or None). A
     tensor is contiguous, on CUDA device `dev`, and of that type and shape."""
     for name, t, dtypes, shape in wanted:
-        if t is not None and not (isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == dev and
-                                  t.dtype in dtypes and t.is_contiguous() and (shape is None or t.shape == shape)):
+        # (get_device is -1 for host tensors)
+        if t is not None and not (isinstance(t, torch.Tensor) and t.get_device() == dev >= 0 and t.dtype in dtypes and
+                                  t.is_contiguous() and (shape is None or t.shape == shape)):
             _refuse(where, f"{name} {_why_not(t, dtypes, dev, shape if shape is not None else ())}")
 
 
