@@ -703,31 +703,26 @@ __device__ __forceinline__ void store_scalars(const LinearParams& p, int64_t row
 }
 
 // Bias, activation and residual of 16 channels from n of a row: y, with u its
-// other half where gated. One choice of the activation for all channels: a
-// branch for each cost more than the products of a 2048-channel layer (503
-// against 1260 TFLOP/s).
+// other half where gated. WHOLE: rows are multiples of 8 channels.
+template <int ACT, bool WHOLE>
 __device__ __forceinline__ void finish16(const LinearParams& p, int g, int64_t row, int n, float (&y)[16], const float (&u)[16]) {
     const float* bias = p.bias ? p.bias + (int64_t)g * p.wide + n : nullptr;
     if (bias) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) y[i] += n + i < p.N ? bias[i] : 0.f;
     }
-    if (p.act == EP_ACT_SWIGLU) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < 16; ++i) {
+        if (ACT == EP_ACT_SWIGLU)
             y[i] = activate(EP_ACT_SILU, y[i]) * (u[i] + (bias && n + i < p.N ? bias[p.N + i] : 0.f));
-    } else if (p.act == EP_ACT_SILU) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = activate(EP_ACT_SILU, y[i]);
-    } else if (p.act == EP_ACT_GELU) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = activate(EP_ACT_GELU, y[i]);
+        else
+            y[i] = activate(ACT, y[i]);
     }
     if (p.res) {
         const uint16_t* r = p.res + row * p.N + n;
 #pragma unroll
         for (int i = 0; i < 16; i += 8) {
-            if (p.N % 8 == 0) {
+            if (WHOLE) {
                 if (n + i >= p.N) continue;
                 const uint4 v = *reinterpret_cast<const uint4*>(r + i);
                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -938,26 +933,81 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             // all warps leave after the same tile: none may wait below for one that left
             ok = epi_sync_and(ok);
-            auto load = [&](int c, float(&z)[16]) {  // 16 channels
-                if (SUM) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float2 v = f32x2_unpack(sum[SUM ? c * 8 + j : 0]);
-                        z[2 * j] = v.x;
-                        z[2 * j + 1] = v.y;
-                    }
-                } else {
-                    uint32_t v[16];
-                    tc::tmem_read16(tmem + lane_base + (acc & 1) * 256 + column(c >> 1) + (c & 1) * 16, v);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) z[j] = __uint_as_float(v[j]);
-                }
-            };
             const bool e4m3 = p.out_type == EP_DTYPE_E4M3;
             const int size = e4m3 ? 1 : p.out_type == EP_DTYPE_FP32 ? 4 : 2;  // bytes of a channel
-            const bool whole = p.N * size % 16 == 0;
             uint4* box = reinterpret_cast<uint4*>(boxes + warp * 4096);
-            float amax = 1e-4f;
+            float amax = 1e-4f, scale = 0.f;
+            // 16 channels, chunk c of the thread's: for the amax (pass 0) or to store
+            auto chunk = [&](auto act, auto whole, int pass, int c, float(&y)[16], const float(&u)[16]) {
+                constexpr int ACT = decltype(act)::value;
+                constexpr bool WHOLE = decltype(whole)::value;
+                const int n = n0 + c * 16;
+                if (n >= p.N) return;
+                if (live) finish16<ACT, WHOLE>(p, g, row, n, y, u);
+                if (pass == 0) {
+                    if (live) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(y[i]));
+                    }
+                } else if (WHOLE) {
+                    const int at = c * size & 7;  // first piece of the chunk
+                    if (live) stage_pieces(box, lane, at, p.out_type, y, scale);
+                    if (at + size == 8 || c == (gated ? 3 : 7) || n + 16 >= p.N)
+                        flush_pieces(p, box, at + size, rows - (warp & 3) * 32, t.row + rank * 128 + (warp & 3) * 32,
+                                     n - at * 16 / size, size);
+                } else if (live) {
+                    store_scalars(p, row, n, y);
+                }
+            };
+            auto chunks = [&](auto act, auto whole, int pass) {
+                if (SUM) {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        if (c >= (gated ? 4 : 8)) continue;
+                        float y[16], u[16];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float2 v = f32x2_unpack(sum[SUM ? c * 8 + j : 0]),
+                                         w = f32x2_unpack(sum[SUM ? (c + 4) % 8 * 8 + j : 0]);
+                            y[2 * j] = v.x;
+                            y[2 * j + 1] = v.y;
+                            u[2 * j] = w.x;
+                            u[2 * j + 1] = w.y;
+                        }
+                        chunk(act, whole, pass, c, y, u);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < (gated ? 4 : 8); ++c) {
+                        float y[16], u[16];
+                        uint32_t v[16];
+                        const uint32_t at = tmem + lane_base + (acc & 1) * 256;
+                        tc::tmem_read16(at + (gated ? half * 64 : half * 128) + c * 16, v);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(v[j]);
+                        if (gated) {
+                            tc::tmem_read16(at + 128 + half * 64 + c * 16, v);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) u[j] = __uint_as_float(v[j]);
+                        }
+                        chunk(act, whole, pass, c, y, u);
+                    }
+                }
+            };
+            // What the epilogue does is chosen here and not for each chunk, and
+            // sums in tensor memory take one loop for all chunks: code that is
+            // run over with most of it skipped waits for instructions (4 of 6 us
+            // of a tile's epilogue).
+            auto pass_of = [&](int pass) {
+                auto with = [&](auto act) {
+                    if (p.N * size % 16 == 0 && p.N % 8 == 0) chunks(act, std::true_type(), pass);
+                    else chunks(act, std::false_type(), pass);
+                };
+                if (p.act == EP_ACT_NONE) with(std::integral_constant<int, EP_ACT_NONE>());
+                else if (p.act == EP_ACT_SILU) with(std::integral_constant<int, EP_ACT_SILU>());
+                else if (p.act == EP_ACT_GELU) with(std::integral_constant<int, EP_ACT_GELU>());
+                else with(std::integral_constant<int, EP_ACT_SWIGLU>());
+            };
             if (ok && rows > (warp & 3) * 32) {
                 // e4m3 goes over the row twice: for its amax, then to store it
 #pragma unroll 1
@@ -969,29 +1019,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     if (pass == 1 && e4m3 && live && (!gated || half == 0) && n0 < p.N)
                         p.out_scale[row * (p.N / 128) + n0 / 128] = amax / 448.0f;
-                    const float scale = 448.0f / amax;
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        if (c >= (gated ? 4 : 8) || n0 + c * 16 >= p.N) continue;
-                        float y[16], u[16];
-                        load(c, y);
-                        if (gated) load((c + 4) & 7, u);
-                        if (live) finish16(p, g, row, n0 + c * 16, y, u);
-                        if (pass == 0) {
-                            if (live) {
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(y[i]));
-                            }
-                        } else if (whole) {
-                            const int at = c * size & 7;  // first piece of the chunk
-                            if (live) stage_pieces(box, lane, at, p.out_type, y, scale);
-                            if (at + size == 8 || c == (gated ? 3 : 7) || n0 + c * 16 + 16 >= p.N)
-                                flush_pieces(p, box, at + size, rows - (warp & 3) * 32,
-                                             t.row + rank * 128 + (warp & 3) * 32, n0 + c * 16 - at * 16 / size, size);
-                        } else if (live) {
-                            store_scalars(p, row, n0 + c * 16, y);
-                        }
-                    }
+                    scale = 448.0f / amax;
+                    pass_of(pass);
                 }
             }
             if (!SUM) {
