@@ -1,0 +1,744 @@
+// The kernels of ep_linear and ep_expert_linear. One source file instantiates
+// them for bf16 operands and one for e4m3, so that they compile side by side.
+#pragma once
+
+#include <type_traits>
+
+#include "linear.cuh"
+
+namespace ep {
+namespace linear {
+namespace {
+
+// BN: rows of x per tile (p.bn).
+template <bool F8, bool SPLIT, int BN>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, LinearParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    const int sb = stage_bytes(p.na, BN);
+    // swizzled tiles start on 1024 bytes (the same offset in every CTA of a cluster)
+    const uint32_t ring = (tc::smem_u32(smem_raw) + 1023) & ~1023u;
+    uint8_t* smem = smem_raw + (ring - tc::smem_u32(smem_raw));
+    uint8_t* after = smem + (size_t)p.stages * sb;
+    float* staging = reinterpret_cast<float*>(after);
+    uint8_t* control = after + (SPLIT ? kInbox : kStaging);
+    float* scales = reinterpret_cast<float*>(control + 512);  // [sets][2][bn]
+    volatile uint32_t* stop = reinterpret_cast<uint32_t*>(control + 500);
+    const uint32_t bars = tc::smem_u32(control);
+    auto full = [&](int s) { return bars + 8 * s; };
+    auto empty = [&](int s) { return bars + 8 * (kMaxStages + s); };
+    auto acc_full = [&](int s) { return bars + 8 * (2 * kMaxStages + s); };
+    auto acc_empty = [&](int s) { return bars + 8 * (2 * kMaxStages + kMaxAcc + s); };
+    auto scale_full = [&](int s) { return bars + 8 * (2 * kMaxStages + 2 * kMaxAcc + s); };
+    const uint32_t drained = bars + 8 * (2 * kMaxStages + 3 * kMaxAcc);
+    auto inbox_full = [&](int b) { return drained + 8 + 8 * b; };
+    auto inbox_free = [&](int b) { return drained + 24 + 8 * b; };
+    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(control + 496);
+    const int sets = 1 << p.acc_log;
+    // set of the acc-th use, the parity of that use's phase, and of the one before it
+    auto set_of = [&](int acc) { return acc & (sets - 1); };
+    auto phase_of = [&](int acc) { return (uint32_t)(acc >> p.acc_log) & 1; };
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            tc::bar_init(full(s), 1);
+            tc::bar_init(empty(s), 1);
+        }
+        for (int s = 0; s < sets; ++s) {
+            tc::bar_init(acc_full(s), 1);
+            tc::bar_init(acc_empty(s), kEpiWarps);
+            tc::bar_init(scale_full(s), 32);
+        }
+        tc::bar_init(drained, 1);
+        for (int b = 0; b < 2; ++b) {
+            tc::bar_init(inbox_full(b), 1);
+            tc::bar_init(inbox_free(b), p.splits);
+        }
+        *stop = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kEpiWarps + 1) tc::tmem_alloc(tc::smem_u32(tmem_at), p.cols);
+    tc::fence_before();
+    __syncthreads();
+    if (SPLIT) tc::cluster_sync();
+    tc::fence_after();
+    const uint32_t tmem = *tmem_at;
+
+    // the CTAs of a cluster take the same tiles, each its part of in_features
+    const int rank = SPLIT ? (int)tc::cluster_rank() : 0;
+    const int first = SPLIT ? blockIdx.x / p.splits : blockIdx.x;
+    const int step = SPLIT ? gridDim.x / p.splits : gridDim.x;
+    const int k_lo = SPLIT ? (int)((int64_t)p.kblocks * rank / p.splits) : 0;
+    const int k_hi = SPLIT ? (int)((int64_t)p.kblocks * (rank + 1) / p.splits) : p.kblocks;
+    constexpr int kElems = F8 ? 128 : 64;  // in_features of a block
+    Cursor cur;
+    Tile t;
+
+    // The loads and products warps run their loops whole and converged; one
+    // elected lane issues.
+    if (warp == kEpiWarps) {  // loads
+        tc::fewer_registers<kOtherRegs>();
+        int i = 0, s = 0;
+        uint32_t wrap = 0;
+        bool ok = true;
+        for (int id = first; ok && find_tile(p, cur, id, t); id += step) {
+            const int subs = subs_of(p, t);
+            const uint32_t bytes = subs * kSub + BN * 128;
+            for (int k = k_lo; k < k_hi; ++k, ++i) {
+                if (wrap > 0) ok = __all_sync(FULL, tc::bar_wait(empty(s), (wrap - 1) & 1, stop));
+                if (!ok) break;
+                if (tc::elect()) {
+                    const uint32_t at = ring + s * sb;
+                    tc::bar_expect(full(s), bytes);
+                    tc::tma_4d(at, &map_w, full(s), k * kElems, channel_of(p, t, 0), 0, t.group / p.R);
+                    if (subs == 2)
+                        tc::tma_4d(at + kSub, &map_w, full(s), k * kElems, channel_of(p, t, 1), p.parts == 2 ? 1 : 0,
+                                   t.group / p.R);
+                    tc::tma_2d(at + p.na * kSub, &map_x, full(s), k * kElems, (int)t.row);
+                }
+                __syncwarp();
+                if (++s == p.stages) {
+                    s = 0;
+                    ++wrap;
+                }
+            }
+            if (!ok && lane == 0)  // copies in flight land before the CTA leaves
+                for (int j = i > p.stages ? i - p.stages : 0; j < i; ++j)
+                    tc::bar_drain(full(j % p.stages), (j / p.stages) & 1);
+        }
+    } else if (warp == kEpiWarps + 1) {  // products
+        tc::fewer_registers<kOtherRegs>();
+        int s = 0, acc = 0;
+        uint32_t wrap = 0;
+        bool ok = true;
+        for (int id = first; ok && find_tile(p, cur, id, t); id += step) {
+            const int subs = subs_of(p, t);
+            const uint32_t idesc = tc::instr_desc(F8, 128, (t.rows + 15) / 16 * 16);
+            int in_set = 0;  // blocks summed in this set so far
+            for (int k = k_lo; k < k_hi; ++k) {
+                if (in_set == 0 && acc >= sets)
+                    ok = __all_sync(FULL, tc::bar_wait(acc_empty(set_of(acc)), phase_of(acc) ^ 1, stop));
+                if (ok) ok = __all_sync(FULL, tc::bar_wait(full(s), wrap & 1, stop));
+                if (!ok) break;
+                tc::fence_after();
+                const uint32_t at = ring + s * sb;
+                const uint64_t b = tc::smem_desc(at + p.na * kSub), w = tc::smem_desc(at);
+                const uint32_t d = tmem + set_of(acc) * p.na * BN;
+                const uint32_t keep = in_set > 0 ? 1u : 0u;
+                const bool last = F8 || in_set == p.flush - 1 || k == k_hi - 1;
+                if (tc::elect()) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)  // 32 bytes of K each
+                        tc::mma<F8>(d, w + 2 * q, b + 2 * q, idesc, q > 0 ? 1u : keep);
+                    if (subs == 2) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            tc::mma<F8>(d + BN, w + kSub / 16 + 2 * q, b + 2 * q, idesc, q > 0 ? 1u : keep);
+                    }
+                    tc::commit(empty(s));
+                    if (last) tc::commit(acc_full(set_of(acc)));
+                }
+                __syncwarp();
+                acc += last;
+                    in_set = last ? 0 : in_set + 1;
+                if (++s == p.stages) {
+                    s = 0;
+                    ++wrap;
+                }
+            }
+            if (!ok) {  // products in flight end before the CTA leaves
+                if (tc::elect()) tc::commit(drained);
+                tc::bar_drain(drained, 0);
+            }
+        }
+    } else if (warp == kEpiWarps + 2) {  // e4m3: row scale x weight block scale of each block and column
+        tc::fewer_registers<kOtherRegs>();
+        if (F8) {
+            int acc = 0;
+            bool ok = true;
+            const int nb = (p.N + 127) / 128;
+            for (int id = first; ok && find_tile(p, cur, id, t); id += step) {
+                const int subs = subs_of(p, t);
+                const float* ws[2];
+#pragma unroll
+                for (int a = 0; a < 2; ++a)
+                    ws[a] = p.w_scale + ((int64_t)(t.group / p.R * p.parts + (p.parts == 2 ? a : 0)) * nb +
+                                         min(channel_of(p, t, a) / 128, nb - 1)) * p.kblocks;
+                // four blocks at a time, loaded four ahead: one load per block
+                // would hold each block up by its latency
+                float xn[BN / 32][4], wn[2][4];
+                auto fetch = [&](int k) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const bool in = k + q < k_hi;
+                        wn[0][q] = in ? ws[0][k + q] : 0.f;
+                        wn[1][q] = in && subs == 2 ? ws[1][k + q] : 0.f;
+#pragma unroll
+                        for (int j = 0; j < BN / 32; ++j)
+                            xn[j][q] = in && lane + 32 * j < t.rows
+                                           ? p.x_scale[(t.row + lane + 32 * j) * p.kblocks + k + q] : 0.f;
+                    }
+                };
+                fetch(k_lo);
+#pragma unroll 1
+                for (int k = k_lo; ok && k < k_hi; k += 4) {
+                    float x4[BN / 32][4], w4[2][4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        w4[0][q] = wn[0][q];
+                        w4[1][q] = wn[1][q];
+#pragma unroll
+                        for (int j = 0; j < BN / 32; ++j) x4[j][q] = xn[j][q];
+                    }
+                    fetch(k + 4);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        if (!ok || k + q >= k_hi) continue;
+                        if (acc >= sets) ok = __all_sync(FULL, tc::bar_wait(acc_empty(set_of(acc)), phase_of(acc) ^ 1, stop));
+                        if (!ok) continue;
+                        float* dst = scales + set_of(acc) * 2 * BN;
+#pragma unroll
+                        for (int j = 0; j < BN / 32; ++j)
+                            if (32 * j < BN) {
+                                dst[lane + 32 * j] = x4[j][q] * w4[0][q];
+                                dst[BN + lane + 32 * j] = x4[j][q] * w4[1][q];
+                            }
+                        tc::bar_arrive(scale_full(set_of(acc)));
+                        ++acc;
+                    }
+                }
+            }
+        }
+    } else if (warp < kEpiWarps) {  // epilogue: warps 0-3 read sub-tile 0, warps 4-7 sub-tile 1
+        tc::more_registers<kEpiRegs>();
+        const int sub = warp >> 2;
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        const int col = sub * 128 + (warp & 3) * 32 + lane;  // channel within a staged row
+        int acc = 0, use = 0;  // accumulator sets, inboxes
+        bool ok = true;
+        for (int id = first; ok && find_tile(p, cur, id, t); id += step) {
+            const int subs = subs_of(p, t);
+            Bias bias;
+            load_bias(p, t, subs, bias);
+            uint64_t sum[BN / 2];  // fp32 pairs: columns 2i, 2i + 1
+#pragma unroll
+            for (int i = 0; i < BN / 2; ++i) sum[i] = 0;
+            for (int k = k_lo; ok && k < k_hi; k += F8 ? 1 : p.flush, ++acc) {
+                ok = tc::bar_wait(acc_full(set_of(acc)), phase_of(acc), stop);
+                if (F8) ok = ok && tc::bar_wait(scale_full(set_of(acc)), phase_of(acc), stop);
+                ok = __all_sync(FULL, ok);
+                if (!ok) break;
+                tc::fence_after();
+                if (sub < subs) {
+                    const ulonglong2* sc = reinterpret_cast<const ulonglong2*>(scales + (set_of(acc) * 2 + sub) * BN);
+                    const uint32_t at = tmem + lane_base + (set_of(acc) * p.na + sub) * BN;
+                    const uint64_t one = f32x2_pack(1.f, 1.f);
+#pragma unroll
+                    for (int c = 0; c < BN / 32; ++c) {
+                        if (c * 32 >= t.rows) continue;
+                        uint32_t v[32];
+                        tc::tmem_ld32(at + c * 32, v);
+                        tc::tmem_ld_wait(v);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            ulonglong2 s2 = make_ulonglong2(one, one);
+                            if (F8) s2 = sc[c * 8 + j];
+                            sum[c * 16 + 2 * j] =
+                                f32x2_fma_rn(f32x2_pack(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1])), s2.x,
+                                             sum[c * 16 + 2 * j]);
+                            sum[c * 16 + 2 * j + 1] =
+                                f32x2_fma_rn(f32x2_pack(__uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3])),
+                                             s2.y, sum[c * 16 + 2 * j + 1]);
+                        }
+                    }
+                }
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) tc::bar_arrive(acc_empty(set_of(acc)));
+            }
+            const int width = subs * 128;
+            // all warps leave after the same tile: none may wait below for one that left
+            ok = epi_sync_and(ok);
+            // the rows of a chunk that are this CTA's: rank, rank + splits, ...
+            const int slots = (32 + p.splits - 1) / p.splits;  // of a CTA, at most
+#pragma unroll 1
+            for (int c = 0; c * 32 < t.rows; ++c) {
+                const int rows = min(32, t.rows - c * 32), b = use & 1;
+                const int own = SPLIT ? (rows + p.splits - 1 - rank) / p.splits : rows;  // this CTA's
+                const float* box = staging + (SPLIT ? b * (kInbox / 8) : 0);
+                if (SPLIT) {
+                    // Row r of the chunk belongs to CTA r % splits. All CTAs push
+                    // their sums of it into that one's inbox, which adds them in
+                    // the order of the CTAs. Two inboxes alternate.
+                    if (use >= 2) ok = tc::bar_wait(inbox_free(b), (use / 2 - 1) & 1, stop) && ok;
+                    if (threadIdx.x == 0)
+                        tc::bar_expect(inbox_full(b), own * p.splits * width * 4);
+                } else if (c > 0) {
+                    epi_sync();  // staging is free
+                }
+                if (ok && sub < subs) {
+                    const uint32_t to = tc::smem_u32(box) + ((SPLIT ? rank * slots * width : 0) + col) * 4;
+                    int owner = 0;
+                    uint32_t at = to;
+#pragma unroll
+                    for (int q = 0; q < BN / 32; ++q) {
+                        if (c != q) continue;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const float2 f = f32x2_unpack(sum[q * 16 + j / 2]);
+                            const float v = j & 1 ? f.y : f.x;
+                            if (!SPLIT) {
+                                staging[j * width + col] = v;
+                                continue;
+                            }
+                            if (j < rows)
+                                tc::push(tc::peer_smem(at, owner), __float_as_uint(v), tc::peer_smem(inbox_full(b), owner));
+                            if (++owner == p.splits) {
+                                owner = 0;
+                                at += width * 4;
+                            }
+                        }
+                    }
+                }
+                if (SPLIT) {
+                    ok = tc::bar_wait(inbox_full(b), (use / 2) & 1, stop) && ok;
+                    ok = epi_sync_and(ok);
+                } else {
+                    epi_sync();
+                }
+                if (ok)
+                    emit_chunk(p, t, subs, bias, warp, own, t.row + c * 32 + (SPLIT ? rank + warp * p.splits : warp),
+                               SPLIT ? p.splits : 1, [&](int i, int s) {
+                                   const float* from = box + i * width + s * 128 + lane * 4;
+                                   float4 a = *reinterpret_cast<const float4*>(from);
+                                   if (SPLIT)
+                                       for (int q = 1; q < p.splits; ++q) {
+                                           const float4 w = *reinterpret_cast<const float4*>(from + q * slots * width);
+                                           a = make_float4(a.x + w.x, a.y + w.y, a.z + w.z, a.w + w.w);
+                                       }
+                                   return a;
+                               });
+                if (SPLIT) {
+                    epi_sync();
+                    if (threadIdx.x < p.splits) tc::bar_arrive_at(tc::peer_smem(inbox_free(b), threadIdx.x));
+                    ++use;
+                }
+            }
+        }
+    } else {
+        tc::fewer_registers<kOtherRegs>();
+    }
+    __syncwarp();
+    __syncthreads();
+    if (SPLIT) tc::cluster_sync();  // no CTA leaves while another may push into its inbox
+    if (threadIdx.x == 0 && *stop) set_error(p.err, EP_DEVERR_TIMEOUT);
+    if (warp == kEpiWarps + 1) tc::tmem_free(tmem, p.cols);
+}
+
+// ---- many rows per group: pairs of CTAs ------------------------------------------
+// The product the other way round, x W^T: 256 rows of x are the lanes (128 in
+// each CTA of the pair), 256 rows of W the columns (gate and up of 128
+// channels, or 256 channels; each CTA loads 128 of them and both use all). A
+// CTA then moves 32 KB into shared memory for 256 x 128 sums of a 64-channel
+// block and the tensor cores read 8 KB per 16 channels, half of what they
+// read for two products of 128 x 128; shared memory is what bounds those. A
+// thread owns a row: its e4m3 scale is one register, and the epilogue needs no
+// exchange but the amax of an e4m3 row between two warps.
+
+
+// A warp's outputs go through 4 KB of shared memory: each lane puts 16-byte
+// pieces of its row there (32 rows of 128 bytes), and the warp stores whole
+// rows' pieces together. Lanes that store their own rows touch 32 lines with
+// each instruction, which took 2.5 to 6.6 us for a tile.
+// Pieces of a row are swapped by row & 7, so that neither side meets in banks.
+__device__ __forceinline__ void stage_pieces(uint4* box, int r, int at, int out_type, const float (&y)[16], float scale) {
+    uint4* row = box + r * 8;
+    const int x = r & 7;
+    if (out_type == EP_DTYPE_E4M3) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            w[j] = pack_e4m3x2(y[4 * j] * scale, y[4 * j + 1] * scale) |
+                   pack_e4m3x2(y[4 * j + 2] * scale, y[4 * j + 3] * scale) << 16;
+        row[at ^ x] = make_uint4(w[0], w[1], w[2], w[3]);
+    } else if (out_type == EP_DTYPE_FP32) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            row[(at + i) ^ x] = make_uint4(__float_as_uint(y[4 * i]), __float_as_uint(y[4 * i + 1]),
+                                           __float_as_uint(y[4 * i + 2]), __float_as_uint(y[4 * i + 3]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            row[(at + i) ^ x] = make_uint4(pack_bf16x2(y[8 * i], y[8 * i + 1]), pack_bf16x2(y[8 * i + 2], y[8 * i + 3]),
+                                           pack_bf16x2(y[8 * i + 4], y[8 * i + 5]), pack_bf16x2(y[8 * i + 6], y[8 * i + 7]));
+    }
+}
+// Stores `pieces` of each of the warp's first `rows` rows, channels from n;
+// rows start at `row`. size: bytes of a channel; size * out_features is a multiple of 16.
+__device__ __forceinline__ void flush_pieces(const LinearParams& p, const uint4* box, int pieces, int rows, int64_t row,
+                                             int n, int size) {
+    const int lane = threadIdx.x & 31, piece = lane & 7;
+    __syncwarp();
+    const bool on = piece < pieces && n + piece * (16 / size) < p.N;
+    uint8_t* out = static_cast<uint8_t*>(p.out) + ((row + lane / 8) * p.N + n) * size + piece * 16;
+    const int64_t step = (int64_t)4 * p.N * size;
+#pragma unroll 2
+    for (int i = 0; i < 8; ++i) {
+        const int r = i * 4 + lane / 8;
+        if (on && r < rows) *reinterpret_cast<uint4*>(out + i * step) = box[r * 8 + (piece ^ (r & 7))];
+    }
+    __syncwarp();
+}
+// The same values one by one, for rows that are no multiple of 16 bytes.
+__device__ __forceinline__ void store_scalars(const LinearParams& p, int64_t row, int n, const float (&y)[16]) {
+    const int64_t at = row * p.N + n;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        if (n + i >= p.N) continue;
+        if (p.out_type == EP_DTYPE_FP32) static_cast<float*>(p.out)[at + i] = y[i];
+        else static_cast<uint16_t*>(p.out)[at + i] = (uint16_t)(pack_bf16x2(y[i], 0.f) & 0xffff);
+    }
+}
+
+// Bias, activation and residual of 16 channels from n of a row: y, with u its
+// other half where gated. WHOLE: rows are multiples of 8 channels.
+template <int ACT, bool WHOLE>
+__device__ __forceinline__ void finish16(const LinearParams& p, int g, int64_t row, int n, float (&y)[16], const float (&u)[16]) {
+    const float* bias = p.bias ? p.bias + (int64_t)g * p.wide + n : nullptr;
+    if (bias) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[i] += n + i < p.N ? bias[i] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        if (ACT == EP_ACT_SWIGLU)
+            y[i] = activate(EP_ACT_SILU, y[i]) * (u[i] + (bias && n + i < p.N ? bias[p.N + i] : 0.f));
+        else
+            y[i] = activate(ACT, y[i]);
+    }
+    if (p.res) {
+        const uint16_t* r = p.res + row * p.N + n;
+#pragma unroll
+        for (int i = 0; i < 16; i += 8) {
+            if (WHOLE) {
+                if (n + i >= p.N) continue;
+                const uint4 v = *reinterpret_cast<const uint4*>(r + i);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    y[i + 2 * j] += bf16lo(w[j]);
+                    y[i + 2 * j + 1] += bf16hi(w[j]);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (n + i + j < p.N) y[i + j] += __uint_as_float((uint32_t)r[i + j] << 16);
+            }
+        }
+    }
+}
+
+// SUM: the sums leave tensor memory in parts, into registers; otherwise whole,
+// by the chunk that the epilogue works on (p.flush is then kblocks).
+template <bool F8, bool SUM>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    linear_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                       LinearParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t ring = (tc::smem_u32(smem_raw) + 1023) & ~1023u;
+    uint8_t* boxes = smem_raw + (ring - tc::smem_u32(smem_raw)) + kPairStages * kPairStage;
+    uint8_t* control = boxes + kEpiWarps * 4096;
+    float* row_amax = reinterpret_cast<float*>(control + 256);  // [2][128]
+    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(control + 240);
+    volatile uint32_t* stop = reinterpret_cast<uint32_t*>(control + 244);
+    const uint32_t bars = tc::smem_u32(control);
+    auto full = [&](int s) { return bars + 8 * s; };  // the leader's are used
+    auto empty = [&](int s) { return bars + 8 * (kPairStages + s); };
+    auto acc_full = [&](int s) { return bars + 8 * (2 * kPairStages + s); };
+    auto acc_empty = [&](int s) { return bars + 8 * (2 * kPairStages + 2 + s); };  // the leader's are used
+    const uint32_t drained = bars + 8 * (2 * kPairStages + 4);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)tc::cluster_rank();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kPairStages; ++s) {
+            tc::bar_init(full(s), 1);
+            tc::bar_init(empty(s), 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            tc::bar_init(acc_full(s), 1);
+            tc::bar_init(acc_empty(s), 2 * kEpiWarps);
+        }
+        tc::bar_init(drained, 1);
+        *stop = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kEpiWarps + 1) tc::pair_tmem_alloc(tc::smem_u32(tmem_at), 512);
+    tc::fence_before();
+    __syncthreads();
+    tc::cluster_sync();
+    tc::fence_after();
+    const uint32_t tmem = *tmem_at;
+    const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    constexpr int kElems = F8 ? 128 : 64;
+    Cursor cur;
+    Tile t;
+
+    if (warp == kEpiWarps) {  // loads, each CTA its halves
+        tc::fewer_registers<kPairOtherRegs>();
+        int i = 0, s = 0;
+        uint32_t wrap = 0;
+        bool ok = true;
+        for (int id = first; ok && find_tile(p, cur, id, t); id += step) {
+            const int ch = p.parts == 2 ? t.n * 128 : t.n * 256 + rank * 128, part = p.parts == 2 ? rank : 0;
+            for (int k = 0; k < p.kblocks; ++k, ++i) {
+                if (wrap > 0) ok = __all_sync(FULL, tc::bar_wait(empty(s), (wrap - 1) & 1, stop));
+                if (!ok) break;
+                if (tc::elect()) {
+                    const uint32_t at = ring + s * kPairStage, bar = tc::peer_smem(full(s), 0);
+                    if (rank == 0) tc::bar_expect(full(s), 2 * kPairStage);
+                    tc::pair_tma_2d(at, &map_x, bar, k * kElems, (int)t.row + rank * 128);
+                    tc::pair_tma_4d(at + kSub, &map_w, bar, k * kElems, ch, part, t.group / p.R);
+                }
+                __syncwarp();
+                if (++s == kPairStages) {
+                    s = 0;
+                    ++wrap;
+                }
+            }
+            if (!ok && lane == 0 && rank == 0)  // the pair's copies in flight land before it leaves
+                for (int j = i > kPairStages ? i - kPairStages : 0; j < i; ++j)
+                    tc::bar_drain(full(j % kPairStages), (j / kPairStages) & 1);
+        }
+    } else if (warp == kEpiWarps + 1) {  // products, by the leader
+        tc::fewer_registers<kPairOtherRegs>();
+        if (rank == 0) {
+            int s = 0, acc = 0;
+            uint32_t wrap = 0;
+            bool ok = true;
+            const uint32_t idesc = tc::instr_desc(F8, 256, 256);
+            for (int id = first; ok && find_tile(p, cur, id, t); id += step) {
+                int in_set = 0;  // blocks summed in this set so far
+                for (int k = 0; k < p.kblocks; ++k) {
+                    if (in_set == 0 && acc >= 2)
+                        ok = __all_sync(FULL, tc::bar_wait(acc_empty(acc & 1), (acc / 2 - 1) & 1, stop));
+                    if (ok) ok = __all_sync(FULL, tc::bar_wait(full(s), wrap & 1, stop));
+                    if (!ok) break;
+                    tc::fence_after();
+                    const uint32_t at = ring + s * kPairStage;
+                    const uint64_t a = tc::smem_desc(at), w = tc::smem_desc(at + kSub);
+                    const uint32_t d = tmem + (acc & 1) * 256;
+                    const uint32_t keep = in_set > 0 ? 1u : 0u;
+                    const bool last = F8 || in_set == p.flush - 1 || k == p.kblocks - 1;
+                    if (tc::elect()) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)  // 32 bytes of K each
+                            tc::pair_mma<F8>(d, a + 2 * q, w + 2 * q, idesc, q > 0 ? 1u : keep);
+                        tc::pair_commit(empty(s));
+                        if (last) tc::pair_commit(acc_full(acc & 1));
+                    }
+                    __syncwarp();
+                    acc += last;
+                    in_set = last ? 0 : in_set + 1;
+                    if (++s == kPairStages) {
+                        s = 0;
+                        ++wrap;
+                    }
+                }
+                if (!ok) {  // products in flight end before the pair leaves
+                    if (tc::elect()) tc::pair_commit(drained);
+                    tc::bar_drain(drained, 0);
+                }
+            }
+        }
+    } else if (warp < kEpiWarps) {  // epilogue: warps w and w + 4 share 32 rows, half of the channels each
+        tc::more_registers<kPairEpiRegs>();
+        const int half = warp >> 2;
+        const int r = (warp & 3) * 32 + lane;  // row of the CTA's 128
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        const bool gated = p.parts == 2;
+        // column of chunk c: two chunks of gate and two of up, or four neighbours
+        auto column = [&](int c) { return gated ? (c >> 1) * 128 + half * 64 + (c & 1) * 32 : half * 128 + c * 32; };
+        const uint32_t empty_at[2] = {tc::peer_smem(acc_empty(0), 0), tc::peer_smem(acc_empty(1), 0)};
+        int acc = 0;
+        bool ok = true;
+        for (int id = first; ok && find_tile(p, cur, id, t); id += step) {
+            const int rows = min(max(t.rows - rank * 128, 0), 128);  // of this CTA
+            const int64_t row = t.row + rank * 128 + r;
+            const bool live = r < rows;
+            const int g = t.group / p.R;
+            const int n0 = gated ? t.n * 128 + half * 64 : t.n * 256 + half * 128;  // the thread's first channel
+            uint64_t sum[SUM ? 64 : 1];  // fp32 pairs: 32 columns of each chunk
+#pragma unroll
+            for (int i = 0; i < (SUM ? 64 : 1); ++i) sum[i] = 0;
+            // a set's sums, times p0 (first two chunks) or p1, from tensor memory
+            auto take = [&](uint64_t p0, uint64_t p1) {
+                tc::fence_after();
+                if (rows > (warp & 3) * 32) {
+                    const uint32_t at = tmem + lane_base + (acc & 1) * 256;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t v[32];
+                        tc::tmem_ld32(at + column(c), v);
+                        tc::tmem_ld_wait(v);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            sum[SUM ? c * 16 + j : 0] = f32x2_fma_rn(
+                                f32x2_pack(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])),
+                                c < 2 ? p0 : p1, sum[SUM ? c * 16 + j : 0]);
+                    }
+                }
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) tc::bar_arrive_at(empty_at[acc & 1]);
+                ++acc;
+            };
+            if (F8) {
+                const int nb = (p.N + 127) / 128;
+                const float* xs = p.x_scale + (live ? row : t.row) * p.kblocks;
+                const float* w0 = p.w_scale + ((int64_t)g * p.parts * nb + (gated ? t.n : min(t.n * 2 + half, nb - 1))) * p.kblocks;
+                const float* w1 = gated ? w0 + (int64_t)nb * p.kblocks : w0;
+                // row scales four blocks at a time, and four ahead: a load that
+                // its own block waited for cost more than the block's products
+                float x4[4], x_next[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) x_next[q] = q < p.kblocks ? xs[q] : 0.f;
+#pragma unroll 1
+                for (int k0 = 0; ok && k0 < p.kblocks; k0 += 4) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        x4[q] = x_next[q];
+                        x_next[q] = k0 + 4 + q < p.kblocks ? xs[k0 + 4 + q] : 0.f;
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        if (!ok || k0 + q >= p.kblocks) continue;
+                        const float s0 = x4[q] * w0[k0 + q], s1 = x4[q] * w1[k0 + q];
+                        ok = __all_sync(FULL, tc::bar_wait(acc_full(acc & 1), (acc / 2) & 1, stop));
+                        if (!ok) continue;
+                        take(f32x2_pack(s0, s0), f32x2_pack(s1, s1));
+                    }
+                }
+            } else if (!SUM) {
+                ok = __all_sync(FULL, tc::bar_wait(acc_full(acc & 1), (acc / 2) & 1, stop));
+                tc::fence_after();
+            } else {
+                const uint64_t one = f32x2_pack(1.f, 1.f);
+                for (int k = 0; k < p.kblocks; k += p.flush) {
+                    ok = __all_sync(FULL, tc::bar_wait(acc_full(acc & 1), (acc / 2) & 1, stop));
+                    if (!ok) break;
+                    take(one, one);
+                }
+            }
+            // all warps leave after the same tile: none may wait below for one that left
+            ok = epi_sync_and(ok);
+            const bool e4m3 = p.out_type == EP_DTYPE_E4M3;
+            const int size = e4m3 ? 1 : p.out_type == EP_DTYPE_FP32 ? 4 : 2;  // bytes of a channel
+            uint4* box = reinterpret_cast<uint4*>(boxes + warp * 4096);
+            float amax = 1e-4f, scale = 0.f;
+            // 16 channels, chunk c of the thread's: for the amax (pass 0) or to store
+            auto chunk = [&](auto act, auto whole, int pass, int c, float(&y)[16], const float(&u)[16]) {
+                constexpr int ACT = decltype(act)::value;
+                constexpr bool WHOLE = decltype(whole)::value;
+                const int n = n0 + c * 16;
+                if (n >= p.N) return;
+                if (live) finish16<ACT, WHOLE>(p, g, row, n, y, u);
+                if (pass == 0) {
+                    if (live) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(y[i]));
+                    }
+                } else if (WHOLE) {
+                    const int at = c * size & 7;  // first piece of the chunk
+                    if (live) stage_pieces(box, lane, at, p.out_type, y, scale);
+                    if (at + size == 8 || c == (gated ? 3 : 7) || n + 16 >= p.N)
+                        flush_pieces(p, box, at + size, rows - (warp & 3) * 32, t.row + rank * 128 + (warp & 3) * 32,
+                                     n - at * 16 / size, size);
+                } else if (live) {
+                    store_scalars(p, row, n, y);
+                }
+            };
+            auto chunks = [&](auto act, auto whole, int pass) {
+                if (SUM) {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        if (c >= (gated ? 4 : 8)) continue;
+                        float y[16], u[16];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float2 v = f32x2_unpack(sum[SUM ? c * 8 + j : 0]),
+                                         w = f32x2_unpack(sum[SUM ? (c + 4) % 8 * 8 + j : 0]);
+                            y[2 * j] = v.x;
+                            y[2 * j + 1] = v.y;
+                            u[2 * j] = w.x;
+                            u[2 * j + 1] = w.y;
+                        }
+                        chunk(act, whole, pass, c, y, u);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < (gated ? 4 : 8); ++c) {
+                        float y[16], u[16];
+                        uint32_t v[16];
+                        const uint32_t at = tmem + lane_base + (acc & 1) * 256;
+                        tc::tmem_read16(at + (gated ? half * 64 : half * 128) + c * 16, v);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(v[j]);
+                        if (gated) {
+                            tc::tmem_read16(at + 128 + half * 64 + c * 16, v);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) u[j] = __uint_as_float(v[j]);
+                        }
+                        chunk(act, whole, pass, c, y, u);
+                    }
+                }
+            };
+            // What the epilogue does is chosen here and not for each chunk, and
+            // sums in tensor memory take one loop for all chunks: code that is
+            // run over with most of it skipped waits for instructions (4 of 6 us
+            // of a tile's epilogue).
+            auto pass_of = [&](int pass) {
+                auto with = [&](auto act) {
+                    if (p.N * size % 16 == 0 && p.N % 8 == 0) chunks(act, std::true_type(), pass);
+                    else chunks(act, std::false_type(), pass);
+                };
+                if (p.act == EP_ACT_NONE) with(std::integral_constant<int, EP_ACT_NONE>());
+                else if (p.act == EP_ACT_SILU) with(std::integral_constant<int, EP_ACT_SILU>());
+                else if (p.act == EP_ACT_GELU) with(std::integral_constant<int, EP_ACT_GELU>());
+                else with(std::integral_constant<int, EP_ACT_SWIGLU>());
+            };
+            if (ok && rows > (warp & 3) * 32) {
+                // e4m3 goes over the row twice: for its amax, then to store it
+#pragma unroll 1
+                for (int pass = e4m3 ? 0 : 1; pass < 2; ++pass) {
+                    if (pass == 1 && e4m3 && gated) {  // the row's other 64 channels are warp +-4's
+                        row_amax[half * 128 + r] = amax;
+                        asm volatile("bar.sync %0, 64;" ::"r"(2 + (warp & 3)) : "memory");
+                        amax = fmaxf(amax, row_amax[(half ^ 1) * 128 + r]);
+                    }
+                    if (pass == 1 && e4m3 && live && (!gated || half == 0) && n0 < p.N)
+                        p.out_scale[row * (p.N / 128) + n0 / 128] = amax / 448.0f;
+                    scale = 448.0f / amax;
+                    pass_of(pass);
+                }
+            }
+            if (!SUM) {
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) tc::bar_arrive_at(empty_at[acc & 1]);
+                ++acc;
+            }
+        }
+    } else {
+        tc::fewer_registers<kPairOtherRegs>();
+    }
+    __syncwarp();
+    __syncthreads();
+    tc::cluster_sync();
+    if (threadIdx.x == 0 && *stop) set_error(p.err, EP_DEVERR_TIMEOUT);
+    if (warp == kEpiWarps + 1) tc::pair_tmem_free(tmem, 512);
+}
+
+}  // namespace
+}  // namespace linear
+}  // namespace ep
