@@ -288,8 +288,8 @@ __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, %0;" ::"n
 constexpr int kPairEpiRegs = 224, kPairOtherRegs = 56;  // as kEpiRegs and kOtherRegs: no e4m3 scales warp here
 static_assert(2 * 128 * kPairEpiRegs + 128 * kPairOtherRegs == kThreads * 168, "register split");
 constexpr int kPairStage = 2 * kSub;
-constexpr int kPairStages = 6;
-constexpr int kPairSmem = kPairStages * kPairStage + kEpiWarps * 4096 + 256 + 2 * 128 * 4 + 1024;
+constexpr int kPairStages = 7;
+constexpr int kPairSmem = kPairStages * kPairStage + 256 + 2 * 128 * 4 + 1024;
 static_assert(kPairSmem <= kSmemMax, "shared memory");
 
 using Kernel = void (*)(CUtensorMap, CUtensorMap, LinearParams);
