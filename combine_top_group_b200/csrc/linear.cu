@@ -221,7 +221,7 @@ ep_status_t launch_on_device(const ep_buffer& b, LinearParams p, int64_t x_rows,
     p.nt = c.nt;
     p.splits = c.splits;
     const int64_t bound = c.bound;
-    if (bound * p.nt >= (int64_t)1 << 30) return fail(EP_ERR_UNSUPPORTED, "too many tiles: rows x out_features");
+    if (bound * p.nt > kMaxTiles) return fail(EP_ERR_UNSUPPORTED, "too many tiles: rows x out_features");
     const bool split = p.splits > 1;
     const int sb = stage_bytes(p.na, p.bn);
     const int fixed = kControl + (split ? kInbox : kStaging) + 1024;  // 1024: alignment of the ring

@@ -46,7 +46,8 @@ struct LinearParams {
     int vec;       // rows of out and residual allow 4-channel accesses
 };
 
-// Rows [start, start + count) of group g, kept inside [0, row_limit).
+// Rows [start, start + count) of group g; none, and an error bit, where they
+// leave [0, row_limit).
 __device__ __forceinline__ void group_rows(const LinearParams& p, int g, int64_t& start, int& count) {
     if (p.off) {
         start = p.off[g];
@@ -58,7 +59,11 @@ __device__ __forceinline__ void group_rows(const LinearParams& p, int g, int64_t
         start = 0;
         count = (int)p.rows;
     }
-    if (start < 0 || count <= 0 || start + count > p.row_limit) count = 0;
+    if (count > 0 && (start < 0 || start + count > p.row_limit)) {
+        set_error(p.err, EP_DEVERR_ROW_BOUNDS);
+        count = 0;
+    }
+    count = max(count, 0);
 }
 
 __device__ __forceinline__ float activate(int act, float z) {
@@ -87,6 +92,8 @@ constexpr int kSmemMax = 227 * 1024;
 
 __host__ __device__ constexpr int stage_bytes(int na, int bn) { return na * kSub + bn * 128; }
 
+constexpr int64_t kMaxTiles = (int64_t)1 << 30;
+
 // Walks the tiles of all groups in order: a group's channel tiles, and within
 // one the row tiles, so that CTAs running together share weights through L2.
 // One warp holds 32 groups at a time.
@@ -112,14 +119,21 @@ __device__ __forceinline__ bool find_tile(const LinearParams& p, Cursor& c, int 
         c.start = 0;
         c.count = 0;
         if (c.g0 + lane < p.G) group_rows(p, c.g0 + lane, c.start, c.count);
-        c.mine = (c.count + p.bn - 1) / p.bn * p.nt;
-        c.incl = c.mine;
+        int64_t incl = (int64_t)((c.count + p.bn - 1) / p.bn) * p.nt;
+        c.mine = (int)incl;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(FULL, c.incl, o);
-            if (lane >= o) c.incl += v;
+            const int64_t v = __shfl_up_sync(FULL, incl, o);
+            if (lane >= o) incl += v;
         }
-        c.total = __shfl_sync(FULL, c.incl, 31);
+        c.incl = (int)incl;
+        const int64_t total = __shfl_sync(FULL, incl, 31);
+        c.total = (int)total;
+        // Rows that overlap can give more tiles than the host allowed for.
+        if (c.base + total > kMaxTiles) {
+            set_error(p.err, EP_DEVERR_ROW_BOUNDS);
+            return false;
+        }
     }
     const int in_window = id - c.base;
     const int src = __ffs(__ballot_sync(FULL, in_window < c.incl)) - 1;

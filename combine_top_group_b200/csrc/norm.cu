@@ -799,7 +799,8 @@ ep_status_t ep_rmsnorm_backward(int64_t N, int H, const void* d_h, const float* 
         const int64_t groups = (N + rps - 1) / rps;
         int per = 0, sms = 0;
         int64_t ctas = resident((const void*)kernel, threads, smem, &per, &sms);
-        if (ctas > kMaxSlots) ctas = kMaxSlots;
+        const int64_t rows = bwd_slots(N, p.tpr);  // what the workspace holds
+        if (ctas > rows) ctas = rows;
         if (groups < ctas) ctas = groups;
         if (ctas > 0) {
             kernel<<<(unsigned)ctas, threads, smem, s>>>(ps);

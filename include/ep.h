@@ -549,7 +549,8 @@ ep_status_t ep_linear(ep_buffer_t *buf, int64_t rows, const ep_linear_t *p, void
  * but reach no output. Rows that hold no slot are left as they were in out and
  * out_scale. T is that of the last ep_get_layout or ep_shard_layout.
  * Errors: EP_ERR_INVALID, EP_ERR_UNSUPPORTED. A wait inside the kernel that
- * gave up sets EP_DEVERR_TIMEOUT. */
+ * gave up sets EP_DEVERR_TIMEOUT; an expert whose rows leave the array gets
+ * none of them, and EP_DEVERR_ROW_BOUNDS. */
 ep_status_t ep_expert_linear(ep_buffer_t *buf, int T, const ep_linear_t *p, void *stream);
 
 /* Diagnostic: proves that the library's bounded waits end. Runs, each with a

@@ -254,6 +254,34 @@ def test_shard(ep, rank):
     untouched(o, sc, slice(off[-1], None))
 
 
+@pytest.mark.parametrize("T,bad", [(30, {3: 1000}), (30, {2: -7}), (30, {1: 50, 2: 20}), (2000, {4: 2 ** 30})])
+def test_bad_offsets(ep, T, bad):
+    """Row offsets that leave the array are reported and reach no memory
+    outside it; the other experts' rows come out as they should."""
+    E, cin, cout = 4, 128, 256
+    buf = buffer(ep, 1, T, E, 1)
+    idx = (torch.arange(T, device=DEV, dtype=torch.int32) * E // T).view(T, 1).contiguous()
+    ep.ep_get_layout(buf, T, topk_idx=idx, topk_w=torch.ones(T, 1, device=DEV))
+    off = ep.ep_buffer_layout(buf, T)["expert_off"]
+    for i, v in bad.items():
+        off[i] = v
+    now = off.tolist()
+    s = operands(3, "bf16", T, E, cin, cout, 0, False, False)
+    o, _ = outputs(T, cout, "bf16")
+    ep.ep_expert_linear(buf, T, s["x"], s["w"], o)
+    wrong = [g for g in range(E) if now[g + 1] > now[g] and (now[g] < 0 or now[g + 1] > T)]
+    assert ep.ep_check_errors(buf) == (ep.EP_DEVERR_ROW_BOUNDS if wrong else 0)
+    kept = [g for g in range(E) if 0 <= now[g] < now[g + 1] <= T]
+    spans = [(now[g], now[g + 1]) for g in kept]
+    for g, (a, b) in zip(kept, spans):
+        if not any(c < b and a < d for c, d in spans if (c, d) != (a, b)):
+            check(s, o, None, a, b - a, g, 0, cout, "bf16")
+    covered = torch.zeros(T + 64, dtype=torch.bool)
+    for a, b in spans:
+        covered[a:b] = True
+    untouched(o, None, (~covered).to(DEV))
+
+
 def test_residual_in_place(ep):
     rows, cin, cout = 70, 192, 100
     s = operands(7, "bf16", rows, 1, cin, cout, 2, True, True)

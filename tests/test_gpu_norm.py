@@ -63,6 +63,16 @@ def test_forward(ep, n, h, gamma_type, residual):
         untouched(w)
 
 
+@pytest.mark.parametrize("n,h", [(37889, 128), (20000, 256), (9500, 384), (9473, 512), (4800, 640), (4737, 1024), (1300, 2176),
+                                 (700, 7168), (3000, 7168), (601, 8192), (700, 8320), (600, 16384), (1201, 12416)])
+@pytest.mark.parametrize("residual", [False, True])
+def test_forward_on_many_rows(ep, n, h, residual):
+    """Rows enough for persistent CTAs that stream them."""
+    test_forward(ep, n, h, F32, residual)
+    if n * h < 1 << 23:
+        test_forward(ep, n, h, BF, residual)
+
+
 @pytest.mark.parametrize("outputs", [("h",), ("y",), ("q", "q_scale"), ("rstd",), ("h", "q", "q_scale")])
 def test_any_outputs(ep, outputs):
     """Each set of outputs gives the bits that all of them together give."""
@@ -133,7 +143,7 @@ def test_in_place(ep, place):
     assert torch.equal(a[place], ho) and torch.equal(y2, y)
 
 
-BACK = [(1, 128), (2, 7168), (517, 1024), (40, 384), (3, 8320), (2, 65536), (3000, 256), (1, 4096)]
+BACK = [(20000, 128), (5000, 1536), (1500, 7168), (700, 12416), (1, 128), (2, 7168), (517, 1024), (40, 384), (3, 8320), (2, 65536), (3000, 256), (1, 4096)]
 
 
 @pytest.mark.parametrize("n,h", BACK)
