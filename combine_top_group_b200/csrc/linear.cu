@@ -205,6 +205,22 @@ Shape shape_of(const ep_buffer& b, const LinearParams& p, int64_t avg, int64_t m
     return c;
 }
 
+// The register split of the kernels waits forever if a launch brings fewer
+// registers than it moves around, so they are counted before the first launch.
+bool has_registers(Kernel kernel) {
+    static std::atomic<Kernel> known[32];
+    for (auto& k : known) {
+        const Kernel at = k.load(std::memory_order_relaxed);
+        if (at == kernel) return true;
+        if (at) continue;
+        cudaFuncAttributes a{};
+        if (cudaFuncGetAttributes(&a, kernel) != cudaSuccess || a.numRegs < 168) return false;
+        k.store(kernel, std::memory_order_relaxed);
+        return true;
+    }
+    return false;
+}
+
 // Chooses tile, split and grid and launches. x_rows: rows that x holds;
 // weights: matrices in w; avg: rows of a group to expect (any count is right).
 ep_status_t launch_on_device(const ep_buffer& b, LinearParams p, int64_t x_rows, int weights, int64_t avg, int64_t most,
@@ -224,13 +240,13 @@ ep_status_t launch_on_device(const ep_buffer& b, LinearParams p, int64_t x_rows,
     if (bound * p.nt > kMaxTiles) return fail(EP_ERR_UNSUPPORTED, "too many tiles: rows x out_features");
     const bool split = p.splits > 1;
     const int sb = stage_bytes(p.na, p.bn);
-    const int fixed = kControl + (split ? kInbox : kStaging) + 1024;  // 1024: alignment of the ring
+    const int fixed = kControl + (split ? kInbox : kStaging);
     p.stages = (kSmemMax - fixed) / sb;
     if (p.stages > kMaxStages) p.stages = kMaxStages;
     const int smem = p.stages * sb + fixed;
     // a set fills while another is read; e4m3 hands one over for each block, and
     // more of them hide the hand-over
-    const int sets = p.na * p.bn <= 64 ? 8 : p.na * p.bn <= 128 ? 4 : 2;
+    const int sets = pair ? 2 : 256 / p.bn;
     p.acc_log = sets == 8 ? 3 : sets == 4 ? 2 : 1;
     p.cols = sets * p.na * p.bn;
 
@@ -244,6 +260,7 @@ ep_status_t launch_on_device(const ep_buffer& b, LinearParams p, int64_t x_rows,
         return fail(EP_ERR_UNSUPPORTED, "x or w is too large for a tensor map");
 
     const Kernel kernel = f8 ? e4m3_kernel(pair, split, p.bn) : bf16_kernel(pair, split, p.bn, p.flush < p.kblocks);
+    if (!has_registers(kernel)) return fail(EP_ERR_CUDA, "the linear kernel was built with fewer than 168 registers");
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
     if (e != cudaSuccess) return fail(EP_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     const int64_t tiles = bound * p.nt, pairs = b.sm_count / 2, clusters = split ? clusters_of(b, p.splits) : 0;

@@ -86,7 +86,7 @@ constexpr int kMaxStages = 10;
 constexpr int kStaging = 32 * 256 * 4;
 constexpr int kInbox = 2 * 36 * 256 * 4;        // a cluster's: 2 x at most 36 rows (splits x rows of each)
 constexpr int kMaxAcc = 8;                      // accumulator sets in tensor memory
-constexpr int kScales = 1024 * 4;               // [sets][2][bn]
+constexpr int kScales = 512 * 4;                // [sets][2][bn]: sets * bn is at most 256
 constexpr int kControl = 512 + kScales;
 constexpr int kSmemMax = 227 * 1024;
 

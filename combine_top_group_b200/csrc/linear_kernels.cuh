@@ -21,7 +21,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // swizzled tiles start on 1024 bytes (the same offset in every CTA of a cluster)
     const uint32_t ring = (tc::smem_u32(smem_raw) + 1023) & ~1023u;
     uint8_t* smem = smem_raw + (ring - tc::smem_u32(smem_raw));
-    uint8_t* after = smem + (size_t)p.stages * sb;
+    // the host counts on shared memory that starts so; if not, a stage makes room
+    const int stages = ring == tc::smem_u32(smem_raw) ? p.stages : p.stages - 1;
+    uint8_t* after = smem + (size_t)stages * sb;
     float* staging = reinterpret_cast<float*>(after);
     uint8_t* control = after + (SPLIT ? kInbox : kStaging);
     float* scales = reinterpret_cast<float*>(control + 512);  // [sets][2][bn]
@@ -43,7 +45,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < p.stages; ++s) {
+        for (int s = 0; s < stages; ++s) {
             tc::bar_init(full(s), 1);
             tc::bar_init(empty(s), 1);
         }
@@ -100,14 +102,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc::tma_2d(at + p.na * kSub, &map_x, full(s), k * kElems, (int)t.row);
                 }
                 __syncwarp();
-                if (++s == p.stages) {
+                if (++s == stages) {
                     s = 0;
                     ++wrap;
                 }
             }
             if (!ok && lane == 0)  // copies in flight land before the CTA leaves
-                for (int j = i > p.stages ? i - p.stages : 0; j < i; ++j)
-                    tc::bar_drain(full(j % p.stages), (j / p.stages) & 1);
+                for (int j = i > stages ? i - stages : 0; j < i; ++j)
+                    tc::bar_drain(full(j % stages), (j / stages) & 1);
         }
     } else if (warp == kEpiWarps + 1) {  // products
         tc::fewer_registers<kOtherRegs>();
@@ -144,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 acc += last;
                     in_set = last ? 0 : in_set + 1;
-                if (++s == p.stages) {
+                if (++s == stages) {
                     s = 0;
                     ++wrap;
                 }

@@ -227,6 +227,44 @@ def test_low_latency_regions(ep, kind, R, T, E, K):
             untouched(o, sc, slice(at + n, at + region))
 
 
+def test_dedup_rows(ep):
+    """The rows that the local permutation of a deduplicated receive lays out."""
+    R, T, E, K, H, cout = 2, 30, 8, 3, 256, 128
+    buf = buffer(ep, R, T, E, K, ep.EP_FLAG_DEDUP, H)
+    idx, wt = routed(9, R * T, E, K)
+    ep.ep_get_layout(buf, T, topk_idx=idx, topk_w=wt)
+    ep.ep_dispatch_dedup(buf, T, torch.randn(R * T, H, generator=gen(1), device=DEV).to(BF))
+    ep.ep_permute(buf, T)
+    x = ep.ep_buffer_recv(buf)["recv_x"]
+    s = dict(operands(5, "bf16", 1, E, H, cout, 1, True, False), x=x)
+    o, _ = outputs(R * T * K, cout, "bf16")
+    ep.ep_expert_linear(buf, T, x, s["w"], o, bias=s["bias"], act=1)
+    assert ep.ep_check_errors(buf) == 0
+    off = ep.ep_buffer_layout(buf, T)["expert_off"].tolist()
+    for g in range(E):
+        check(s, o, None, off[g], off[g + 1] - off[g], g, 1, cout, "bf16")
+    untouched(o, None, slice(off[-1], None))
+
+
+def test_large_calls_on_two_streams(ep):
+    """Calls that each take every SM, with pairs and with clusters, at once."""
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    sets = []
+    for seed, (rows, cin, cout, st) in enumerate(((3000, 1024, 4096, s1), (40, 8192, 2048, s2), (700, 2048, 512, s1), (300, 4096, 1024, s2))):
+        s = operands(seed, "bf16", rows, 1, cin, cout, 0, False, False)
+        want, got = torch.empty(rows, cout, dtype=BF, device=DEV), torch.empty(rows, cout, dtype=BF, device=DEV)
+        sets.append((buffer(ep, 1, 1, 1, 1), s, want, got, st))
+    for buf, s, want, _, _ in sets:
+        ep.ep_linear(buf, s["x"], s["w"], want)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for buf, s, _, got, st in sets:
+            ep.ep_linear(buf, s["x"], s["w"], got, stream=st)
+    torch.cuda.synchronize()
+    for buf, _, want, got, _ in sets:
+        assert torch.equal(want, got) and ep.ep_check_errors(buf) == 0
+
+
 @pytest.mark.parametrize("rank", [0, 3])
 def test_shard(ep, rank):
     """A shard's own experts on the rows that all ranks send it."""
