@@ -209,7 +209,7 @@ def test_a_row_stays_apart(ep, bad):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
-@pytest.mark.parametrize("R,T,E,K", [(2, 12, 8, 2), (4, 33, 4, 2), (8, 16, 64, 6)])
+@pytest.mark.parametrize("R,T,E,K", [(2, 12, 8, 2), (4, 33, 4, 2), (8, 16, 64, 6), (2, 900, 4, 2), (1, 1500, 2, 1)])
 def test_low_latency_regions(ep, kind, R, T, E, K):
     buf = buffer(ep, R, T + 3, E, K, ep.EP_FLAG_LOW_LATENCY)
     idx, wt = routed(1, R * T, E, K, hot=0.5)
