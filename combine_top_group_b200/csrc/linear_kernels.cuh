@@ -592,8 +592,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 float x4[4], x_next[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) x_next[q] = q < p.kblocks ? xs[q] : 0.f;
+                // block scales: 32 blocks' at a time, one to a lane
+                float w0_lane = 0.f, w1_lane = 0.f;
 #pragma unroll 1
                 for (int k0 = 0; ok && k0 < p.kblocks; k0 += 4) {
+                    if ((k0 & 31) == 0 && k0 + lane < p.kblocks) {
+                        w0_lane = w0[k0 + lane];
+                        w1_lane = w1[k0 + lane];
+                    }
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         x4[q] = x_next[q];
@@ -602,7 +608,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         if (!ok || k0 + q >= p.kblocks) continue;
-                        const float s0 = x4[q] * w0[k0 + q], s1 = x4[q] * w1[k0 + q];
+                        const int at = (k0 & 31) + q;
+                        const float s0 = x4[q] * __shfl_sync(FULL, w0_lane, at), s1 = x4[q] * __shfl_sync(FULL, w1_lane, at);
                         ok = __all_sync(FULL, tc::bar_wait(acc_full(acc & 1), (acc / 2) & 1, stop));
                         if (!ok) continue;
                         take(f32x2_pack(s0, s0), f32x2_pack(s1, s1));
