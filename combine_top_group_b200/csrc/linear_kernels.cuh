@@ -80,141 +80,138 @@ __global__ void __launch_bounds__(kThreads, 1)
     Tile t;
 
     // The loads and products warps run their loops whole and converged; one
-    // elected lane issues.
-    if (warp == kEpiWarps) {  // loads
+    // elected lane issues. A warpgroup changes its registers by one instruction
+    // that all its warps execute, before they part.
+    if (warp >= kEpiWarps) {
         tc::fewer_registers<kOtherRegs>();
-        int i = 0, s = 0;
-        uint32_t wrap = 0;
-        bool ok = true;
-        for (int id = first; ok && find_tile(p, cur, id, t); id += step) {
-            const int subs = subs_of(p, t);
-            const uint32_t bytes = subs * kSub + BN * 128;
-            for (int k = k_lo; k < k_hi; ++k, ++i) {
-                if (wrap > 0) ok = __all_sync(FULL, tc::bar_wait(empty(s), (wrap - 1) & 1, stop));
-                if (!ok) break;
-                if (tc::elect()) {
-                    const uint32_t at = ring + s * sb;
-                    tc::bar_expect(full(s), bytes);
-                    tc::tma_4d(at, &map_w, full(s), k * kElems, channel_of(p, t, 0), 0, t.group / p.R);
-                    if (subs == 2)
-                        tc::tma_4d(at + kSub, &map_w, full(s), k * kElems, channel_of(p, t, 1), p.parts == 2 ? 1 : 0,
-                                   t.group / p.R);
-                    tc::tma_2d(at + p.na * kSub, &map_x, full(s), k * kElems, (int)t.row);
-                }
-                __syncwarp();
-                if (++s == stages) {
-                    s = 0;
-                    ++wrap;
-                }
-            }
-            if (!ok && lane == 0)  // copies in flight land before the CTA leaves
-                for (int j = i > stages ? i - stages : 0; j < i; ++j)
-                    tc::bar_drain(full(j % stages), (j / stages) & 1);
-        }
-    } else if (warp == kEpiWarps + 1) {  // products
-        tc::fewer_registers<kOtherRegs>();
-        int s = 0, acc = 0;
-        uint32_t wrap = 0;
-        bool ok = true;
-        for (int id = first; ok && find_tile(p, cur, id, t); id += step) {
-            const int subs = subs_of(p, t);
-            const uint32_t idesc = tc::instr_desc(F8, 128, (t.rows + 15) / 16 * 16);
-            int in_set = 0;  // blocks summed in this set so far
-            for (int k = k_lo; k < k_hi; ++k) {
-                if (in_set == 0 && acc >= sets)
-                    ok = __all_sync(FULL, tc::bar_wait(acc_empty(set_of(acc)), phase_of(acc) ^ 1, stop));
-                if (ok) ok = __all_sync(FULL, tc::bar_wait(full(s), wrap & 1, stop));
-                if (!ok) break;
-                tc::fence_after();
-                const uint32_t at = ring + s * sb;
-                const uint64_t b = tc::smem_desc(at + p.na * kSub), w = tc::smem_desc(at);
-                const uint32_t d = tmem + set_of(acc) * p.na * BN;
-                const uint32_t keep = in_set > 0 ? 1u : 0u;
-                const bool last = F8 || in_set == p.flush - 1 || k == k_hi - 1;
-                if (tc::elect()) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)  // 32 bytes of K each
-                        tc::mma<F8>(d, w + 2 * q, b + 2 * q, idesc, q > 0 ? 1u : keep);
-                    if (subs == 2) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            tc::mma<F8>(d + BN, w + kSub / 16 + 2 * q, b + 2 * q, idesc, q > 0 ? 1u : keep);
-                    }
-                    tc::commit(empty(s));
-                    if (last) tc::commit(acc_full(set_of(acc)));
-                }
-                __syncwarp();
-                acc += last;
-                    in_set = last ? 0 : in_set + 1;
-                if (++s == stages) {
-                    s = 0;
-                    ++wrap;
-                }
-            }
-            if (!ok) {  // products in flight end before the CTA leaves
-                if (tc::elect()) tc::commit(drained);
-                tc::bar_drain(drained, 0);
-            }
-        }
-    } else if (warp == kEpiWarps + 2) {  // e4m3: row scale x weight block scale of each block and column
-        tc::fewer_registers<kOtherRegs>();
-        if (F8) {
-            int acc = 0;
+        if (warp == kEpiWarps) {  // loads
+            int i = 0, s = 0;
+            uint32_t wrap = 0;
             bool ok = true;
-            const int nb = (p.N + 127) / 128;
             for (int id = first; ok && find_tile(p, cur, id, t); id += step) {
                 const int subs = subs_of(p, t);
-                const float* ws[2];
-#pragma unroll
-                for (int a = 0; a < 2; ++a)
-                    ws[a] = p.w_scale + ((int64_t)(t.group / p.R * p.parts + (p.parts == 2 ? a : 0)) * nb +
-                                         min(channel_of(p, t, a) / 128, nb - 1)) * p.kblocks;
-                // four blocks at a time, loaded four ahead: one load per block
-                // would hold each block up by its latency
-                float xn[BN / 32][4], wn[2][4];
-                auto fetch = [&](int k) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const bool in = k + q < k_hi;
-                        wn[0][q] = in ? ws[0][k + q] : 0.f;
-                        wn[1][q] = in && subs == 2 ? ws[1][k + q] : 0.f;
-#pragma unroll
-                        for (int j = 0; j < BN / 32; ++j)
-                            xn[j][q] = in && lane + 32 * j < t.rows
-                                           ? p.x_scale[(t.row + lane + 32 * j) * p.kblocks + k + q] : 0.f;
+                const uint32_t bytes = subs * kSub + BN * 128;
+                for (int k = k_lo; k < k_hi; ++k, ++i) {
+                    if (wrap > 0) ok = __all_sync(FULL, tc::bar_wait(empty(s), (wrap - 1) & 1, stop));
+                    if (!ok) break;
+                    if (tc::elect()) {
+                        const uint32_t at = ring + s * sb;
+                        tc::bar_expect(full(s), bytes);
+                        tc::tma_4d(at, &map_w, full(s), k * kElems, channel_of(p, t, 0), 0, t.group / p.R);
+                        if (subs == 2)
+                            tc::tma_4d(at + kSub, &map_w, full(s), k * kElems, channel_of(p, t, 1), p.parts == 2 ? 1 : 0,
+                                       t.group / p.R);
+                        tc::tma_2d(at + p.na * kSub, &map_x, full(s), k * kElems, (int)t.row);
                     }
-                };
-                fetch(k_lo);
-#pragma unroll 1
-                for (int k = k_lo; ok && k < k_hi; k += 4) {
+                    __syncwarp();
+                    if (++s == stages) {
+                        s = 0;
+                        ++wrap;
+                    }
+                }
+                if (!ok && lane == 0)  // copies in flight land before the CTA leaves
+                    for (int j = i > stages ? i - stages : 0; j < i; ++j)
+                        tc::bar_drain(full(j % stages), (j / stages) & 1);
+            }
+        } else if (warp == kEpiWarps + 1) {  // products
+            int s = 0, acc = 0;
+            uint32_t wrap = 0;
+            bool ok = true;
+            for (int id = first; ok && find_tile(p, cur, id, t); id += step) {
+                const int subs = subs_of(p, t);
+                const uint32_t idesc = tc::instr_desc(F8, 128, (t.rows + 15) / 16 * 16);
+                int in_set = 0;  // blocks summed in this set so far
+                for (int k = k_lo; k < k_hi; ++k) {
+                    if (in_set == 0 && acc >= sets)
+                        ok = __all_sync(FULL, tc::bar_wait(acc_empty(set_of(acc)), phase_of(acc) ^ 1, stop));
+                    if (ok) ok = __all_sync(FULL, tc::bar_wait(full(s), wrap & 1, stop));
+                    if (!ok) break;
+                    tc::fence_after();
+                    const uint32_t at = ring + s * sb;
+                    const uint64_t b = tc::smem_desc(at + p.na * kSub), w = tc::smem_desc(at);
+                    const uint32_t d = tmem + set_of(acc) * p.na * BN;
+                    const uint32_t keep = in_set > 0 ? 1u : 0u;
+                    const bool last = F8 || in_set == p.flush - 1 || k == k_hi - 1;
+                    if (tc::elect()) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)  // 32 bytes of K each
+                            tc::mma<F8>(d, w + 2 * q, b + 2 * q, idesc, q > 0 ? 1u : keep);
+                        if (subs == 2) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                tc::mma<F8>(d + BN, w + kSub / 16 + 2 * q, b + 2 * q, idesc, q > 0 ? 1u : keep);
+                        }
+                        tc::commit(empty(s));
+                        if (last) tc::commit(acc_full(set_of(acc)));
+                    }
+                    __syncwarp();
+                    acc += last;
+                    in_set = last ? 0 : in_set + 1;
+                    if (++s == stages) {
+                        s = 0;
+                        ++wrap;
+                    }
+                }
+                if (!ok) {  // products in flight end before the CTA leaves
+                    if (tc::elect()) tc::commit(drained);
+                    tc::bar_drain(drained, 0);
+                }
+            }
+        } else if (warp == kEpiWarps + 2) {  // e4m3: row scale x weight block scale of each block and column
+            if (F8) {
+                int acc = 0;
+                bool ok = true;
+                const int nb = (p.N + 127) / 128;
+                for (int id = first; ok && find_tile(p, cur, id, t); id += step) {
+                    const int subs = subs_of(p, t);
+                    const float* ws[2];
+#pragma unroll
+                    for (int a = 0; a < 2; ++a)
+                        ws[a] = p.w_scale + ((int64_t)(t.group / p.R * p.parts + (p.parts == 2 ? a : 0)) * nb +
+                                             min(channel_of(p, t, a) / 128, nb - 1)) * p.kblocks;
+                    // loaded four blocks ahead: a load that its own block waited
+                    // for would hold that block up by its latency
                     float x4[BN / 32][4], w4[2][4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        w4[0][q] = wn[0][q];
-                        w4[1][q] = wn[1][q];
-#pragma unroll
-                        for (int j = 0; j < BN / 32; ++j) x4[j][q] = xn[j][q];
-                    }
-                    fetch(k + 4);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        if (!ok || k + q >= k_hi) continue;
-                        if (acc >= sets) ok = __all_sync(FULL, tc::bar_wait(acc_empty(set_of(acc)), phase_of(acc) ^ 1, stop));
-                        if (!ok) continue;
-                        float* dst = scales + set_of(acc) * 2 * BN;
+                    auto fetch = [&](int k, int q) {
+                        const bool in = k < k_hi;
+                        w4[0][q] = in ? ws[0][k] : 0.f;
+                        w4[1][q] = in && subs == 2 ? ws[1][k] : 0.f;
 #pragma unroll
                         for (int j = 0; j < BN / 32; ++j)
-                            if (32 * j < BN) {
-                                dst[lane + 32 * j] = x4[j][q] * w4[0][q];
-                                dst[BN + lane + 32 * j] = x4[j][q] * w4[1][q];
+                            x4[j][q] = in && lane + 32 * j < t.rows
+                                           ? p.x_scale[(t.row + lane + 32 * j) * p.kblocks + k] : 0.f;
+                    };
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) fetch(k_lo + q, q);
+#pragma unroll 1
+                    for (int k = k_lo; ok && k < k_hi; k += 4) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            if (!ok || k + q >= k_hi) continue;
+                            float s0[BN / 32], s1[BN / 32];
+#pragma unroll
+                            for (int j = 0; j < BN / 32; ++j) {
+                                s0[j] = x4[j][q] * w4[0][q];
+                                s1[j] = x4[j][q] * w4[1][q];
                             }
-                        tc::bar_arrive(scale_full(set_of(acc)));
-                        ++acc;
+                            fetch(k + 4 + q, q);
+                            if (acc >= sets)
+                                ok = __all_sync(FULL, tc::bar_wait(acc_empty(set_of(acc)), phase_of(acc) ^ 1, stop));
+                            if (!ok) continue;
+                            float* dst = scales + set_of(acc) * 2 * BN + lane;
+#pragma unroll
+                            for (int j = 0; j < BN / 32; ++j) {
+                                dst[32 * j] = s0[j];
+                                dst[BN + 32 * j] = s1[j];
+                            }
+                            tc::bar_arrive(scale_full(set_of(acc)));
+                            ++acc;
+                        }
                     }
                 }
             }
         }
-    } else if (warp < kEpiWarps) {  // epilogue: warps 0-3 read sub-tile 0, warps 4-7 sub-tile 1
+    } else {  // epilogue: warps 0-3 read sub-tile 0, warps 4-7 sub-tile 1
         tc::more_registers<kEpiRegs>();
         const int sub = warp >> 2;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
@@ -330,8 +327,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-    } else {
-        tc::fewer_registers<kOtherRegs>();
     }
     __syncwarp();
     __syncthreads();
@@ -473,74 +468,75 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     Cursor cur;
     Tile t;
 
-    if (warp == kEpiWarps) {  // loads, each CTA its halves
+    if (warp >= kEpiWarps) {
         tc::fewer_registers<kPairOtherRegs>();
-        int i = 0, s = 0;
-        uint32_t wrap = 0;
-        bool ok = true;
-        for (int id = first; ok && find_tile(p, cur, id, t); id += step) {
-            const int ch = p.parts == 2 ? t.n * 128 : t.n * 256 + rank * 128, part = p.parts == 2 ? rank : 0;
-            for (int k = 0; k < p.kblocks; ++k, ++i) {
-                if (wrap > 0) ok = __all_sync(FULL, tc::bar_wait(empty(s), (wrap - 1) & 1, stop));
-                if (!ok) break;
-                if (tc::elect()) {
-                    const uint32_t at = ring + s * kPairStage, bar = tc::peer_smem(full(s), 0);
-                    if (rank == 0) tc::bar_expect(full(s), 2 * kPairStage);
-                    tc::pair_tma_2d(at, &map_x, bar, k * kElems, (int)t.row + rank * 128);
-                    tc::pair_tma_4d(at + kSub, &map_w, bar, k * kElems, ch, part, t.group / p.R);
-                }
-                __syncwarp();
-                if (++s == kPairStages) {
-                    s = 0;
-                    ++wrap;
-                }
-            }
-            if (!ok && lane == 0 && rank == 0)  // the pair's copies in flight land before it leaves
-                for (int j = i > kPairStages ? i - kPairStages : 0; j < i; ++j)
-                    tc::bar_drain(full(j % kPairStages), (j / kPairStages) & 1);
-        }
-    } else if (warp == kEpiWarps + 1) {  // products, by the leader
-        tc::fewer_registers<kPairOtherRegs>();
-        if (rank == 0) {
-            int s = 0, acc = 0;
+        if (warp == kEpiWarps) {  // loads, each CTA its halves
+            int i = 0, s = 0;
             uint32_t wrap = 0;
             bool ok = true;
-            const uint32_t idesc = tc::instr_desc(F8, 256, 256);
             for (int id = first; ok && find_tile(p, cur, id, t); id += step) {
-                int in_set = 0;  // blocks summed in this set so far
-                for (int k = 0; k < p.kblocks; ++k) {
-                    if (in_set == 0 && acc >= 2)
-                        ok = __all_sync(FULL, tc::bar_wait(acc_empty(acc & 1), (acc / 2 - 1) & 1, stop));
-                    if (ok) ok = __all_sync(FULL, tc::bar_wait(full(s), wrap & 1, stop));
+                const int ch = p.parts == 2 ? t.n * 128 : t.n * 256 + rank * 128, part = p.parts == 2 ? rank : 0;
+                for (int k = 0; k < p.kblocks; ++k, ++i) {
+                    if (wrap > 0) ok = __all_sync(FULL, tc::bar_wait(empty(s), (wrap - 1) & 1, stop));
                     if (!ok) break;
-                    tc::fence_after();
-                    const uint32_t at = ring + s * kPairStage;
-                    const uint64_t a = tc::smem_desc(at), w = tc::smem_desc(at + kSub);
-                    const uint32_t d = tmem + (acc & 1) * 256;
-                    const uint32_t keep = in_set > 0 ? 1u : 0u;
-                    const bool last = F8 || in_set == p.flush - 1 || k == p.kblocks - 1;
                     if (tc::elect()) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)  // 32 bytes of K each
-                            tc::pair_mma<F8>(d, a + 2 * q, w + 2 * q, idesc, q > 0 ? 1u : keep);
-                        tc::pair_commit(empty(s));
-                        if (last) tc::pair_commit(acc_full(acc & 1));
+                        const uint32_t at = ring + s * kPairStage, bar = tc::peer_smem(full(s), 0);
+                        if (rank == 0) tc::bar_expect(full(s), 2 * kPairStage);
+                        tc::pair_tma_2d(at, &map_x, bar, k * kElems, (int)t.row + rank * 128);
+                        tc::pair_tma_4d(at + kSub, &map_w, bar, k * kElems, ch, part, t.group / p.R);
                     }
                     __syncwarp();
-                    acc += last;
-                    in_set = last ? 0 : in_set + 1;
                     if (++s == kPairStages) {
                         s = 0;
                         ++wrap;
                     }
                 }
-                if (!ok) {  // products in flight end before the pair leaves
-                    if (tc::elect()) tc::pair_commit(drained);
-                    tc::bar_drain(drained, 0);
+                if (!ok && lane == 0 && rank == 0)  // the pair's copies in flight land before it leaves
+                    for (int j = i > kPairStages ? i - kPairStages : 0; j < i; ++j)
+                        tc::bar_drain(full(j % kPairStages), (j / kPairStages) & 1);
+            }
+        } else if (warp == kEpiWarps + 1) {  // products, by the leader
+            if (rank == 0) {
+                int s = 0, acc = 0;
+                uint32_t wrap = 0;
+                bool ok = true;
+                const uint32_t idesc = tc::instr_desc(F8, 256, 256);
+                for (int id = first; ok && find_tile(p, cur, id, t); id += step) {
+                    int in_set = 0;  // blocks summed in this set so far
+                    for (int k = 0; k < p.kblocks; ++k) {
+                        if (in_set == 0 && acc >= 2)
+                            ok = __all_sync(FULL, tc::bar_wait(acc_empty(acc & 1), (acc / 2 - 1) & 1, stop));
+                        if (ok) ok = __all_sync(FULL, tc::bar_wait(full(s), wrap & 1, stop));
+                        if (!ok) break;
+                        tc::fence_after();
+                        const uint32_t at = ring + s * kPairStage;
+                        const uint64_t a = tc::smem_desc(at), w = tc::smem_desc(at + kSub);
+                        const uint32_t d = tmem + (acc & 1) * 256;
+                        const uint32_t keep = in_set > 0 ? 1u : 0u;
+                        const bool last = F8 || in_set == p.flush - 1 || k == p.kblocks - 1;
+                        if (tc::elect()) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)  // 32 bytes of K each
+                                tc::pair_mma<F8>(d, a + 2 * q, w + 2 * q, idesc, q > 0 ? 1u : keep);
+                            tc::pair_commit(empty(s));
+                            if (last) tc::pair_commit(acc_full(acc & 1));
+                        }
+                        __syncwarp();
+                        acc += last;
+                    in_set = last ? 0 : in_set + 1;
+                        if (++s == kPairStages) {
+                            s = 0;
+                            ++wrap;
+                        }
+                    }
+                    if (!ok) {  // products in flight end before the pair leaves
+                        if (tc::elect()) tc::pair_commit(drained);
+                        tc::bar_drain(drained, 0);
+                    }
                 }
             }
         }
-    } else if (warp < kEpiWarps) {  // epilogue: warps w and w + 4 share 32 rows, half of the channels each
+    } else {  // epilogue: warps w and w + 4 share 32 rows, half of the channels each
         tc::more_registers<kPairEpiRegs>();
         const int half = warp >> 2;
         const int r = (warp & 3) * 32 + lane;  // row of the CTA's 128
@@ -718,8 +714,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 ++acc;
             }
         }
-    } else {
-        tc::fewer_registers<kPairOtherRegs>();
     }
     __syncwarp();
     __syncthreads();

@@ -1,0 +1,41 @@
+"""Rules of the linear kernels that no run can show to be kept: breaking them
+is undefined behaviour that may work by chance. Read off the source (these run
+without a GPU)."""
+import os
+import re
+
+import pytest
+
+from conftest import ROOT
+
+CSRC = os.path.join(ROOT, "combine_top_group_b200", "csrc")
+
+
+def code(name: str) -> str:
+    from combine_top_group_b200 import metrics
+    with open(os.path.join(CSRC, name), encoding="utf-8") as f:
+        return metrics.code_of(f.read())
+
+
+def kernels() -> dict:
+    """Name and code of each kernel of linear_kernels.cuh."""
+    parts = re.split(r"__global__ void ", code("linear_kernels.cuh"))[1:]
+    return {re.search(r"(\w+)\s*\(\s*const __grid_constant__", p)[1]: p for p in parts}
+
+
+def test_kernels_are_found():
+    assert set(kernels()) == {"linear_kernel", "linear_pair_kernel"}
+
+
+@pytest.mark.parametrize("name", ["linear_kernel", "linear_pair_kernel"])
+def test_one_register_instruction_per_warpgroup(name):
+    """All warps of a warpgroup have to execute the same setmaxnreg, so a
+    kernel names it once for the epilogue's warpgroups and once for the other,
+    before that one's warps part. (One in each warp's branch is undefined; the
+    epilogue's request may then wait for registers that nobody gives back.)"""
+    k = kernels()[name]
+    assert len(re.findall(r"more_registers<", k)) == 1
+    assert len(re.findall(r"fewer_registers<", k)) == 1
+    assert re.search(r"if \(warp >= kEpiWarps\) \{ tc::fewer_registers<", k)
+    roles = [m.start() for m in re.finditer(r"if \(warp == kEpiWarps( \+ \d)?\) \{", k)]
+    assert roles and all(k.index("fewer_registers<") < at for at in roles)
