@@ -271,8 +271,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (SPLIT) {
                     // Row r of the chunk belongs to CTA r % splits. All CTAs push
                     // their sums of it into that one's inbox, which adds them in
-                    // the order of the CTAs. Two inboxes alternate.
-                    if (use >= 2) ok = tc::bar_wait(inbox_free(b), (use / 2 - 1) & 1, stop) && ok;
+                    // the order of the CTAs. Two inboxes alternate. Their barriers
+                    // order shared memory between CTAs, at the cluster's scope:
+                    // full after the pushes, free after the reads.
+                    if (use >= 2) ok = tc::bar_wait<tc::kCluster>(inbox_free(b), (use / 2 - 1) & 1, stop) && ok;
                     if (threadIdx.x == 0)
                         tc::bar_expect(inbox_full(b), own * p.splits * width * 4);
                 } else if (c > 0) {
@@ -303,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (SPLIT) {
-                    ok = tc::bar_wait(inbox_full(b), (use / 2) & 1, stop) && ok;
+                    ok = tc::bar_wait<tc::kCluster>(inbox_full(b), (use / 2) & 1, stop) && ok;
                     ok = epi_sync_and(ok);
                 } else {
                     epi_sync();
@@ -322,7 +324,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                });
                 if (SPLIT) {
                     epi_sync();
-                    if (threadIdx.x < p.splits) tc::bar_arrive_at(tc::peer_smem(inbox_free(b), threadIdx.x));
+                    if (threadIdx.x < p.splits)
+                        tc::bar_arrive_at<tc::kCluster>(tc::peer_smem(inbox_free(b), threadIdx.x));
                     ++use;
                 }
             }
@@ -523,7 +526,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         }
                         __syncwarp();
                         acc += last;
-                    in_set = last ? 0 : in_set + 1;
+                        in_set = last ? 0 : in_set + 1;
                         if (++s == kPairStages) {
                             s = 0;
                             ++wrap;

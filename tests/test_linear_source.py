@@ -39,3 +39,19 @@ def test_one_register_instruction_per_warpgroup(name):
     assert re.search(r"if \(warp >= kEpiWarps\) \{ tc::fewer_registers<", k)
     roles = [m.start() for m in re.finditer(r"if \(warp == kEpiWarps( \+ \d)?\) \{", k)]
     assert roles and all(k.index("fewer_registers<") < at for at in roles)
+
+
+def test_inboxes_are_handed_over_at_the_clusters_scope():
+    """The CTAs of a cluster write each other's inboxes in shared memory. The
+    order of those writes and of the reads before and after them rests on the
+    inboxes' barriers, so each arrival and wait on these names the cluster's
+    scope; the default is the CTA's."""
+    k = kernels()["linear_kernel"]
+    for bar in ("inbox_free", "inbox_full"):
+        waits = re.findall(r"bar_wait(<[\w:]+>)?\(" + bar, k)
+        assert waits and set(waits) == {"<tc::kCluster>"}, (bar, waits)
+    arrivals = re.findall(r"bar_arrive\w*(<[\w:]+>)?\([^;]*inbox_free", k)
+    assert arrivals == ["<tc::kCluster>"]
+    ptx = code("tcgen05.cuh")
+    assert "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64" in ptx
+    assert "mbarrier.arrive.release.cluster.shared::cluster.b64" in ptx
