@@ -78,6 +78,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kElems = F8 ? 128 : 64;  // in_features of a block
     Cursor cur;
     Tile t;
+    int loads = 0;  // that the loads warp has issued
 
     // The loads and products warps run their loops whole and converged; one
     // elected lane issues. A warpgroup changes its registers by one instruction
@@ -85,13 +86,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp >= kEpiWarps) {
         tc::fewer_registers<kOtherRegs>();
         if (warp == kEpiWarps) {  // loads
-            int i = 0, s = 0;
+            int s = 0;
             uint32_t wrap = 0;
             bool ok = true;
             for (int id = first; ok && find_tile(p, cur, id, t); id += step) {
                 const int subs = subs_of(p, t);
                 const uint32_t bytes = subs * kSub + BN * 128;
-                for (int k = k_lo; k < k_hi; ++k, ++i) {
+                for (int k = k_lo; k < k_hi; ++k, ++loads) {
                     if (wrap > 0) ok = __all_sync(FULL, tc::bar_wait(empty(s), (wrap - 1) & 1, stop));
                     if (!ok) break;
                     if (tc::elect()) {
@@ -109,9 +110,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ++wrap;
                     }
                 }
-                if (!ok && lane == 0)  // copies in flight land before the CTA leaves
-                    for (int j = i > stages ? i - stages : 0; j < i; ++j)
-                        tc::bar_drain(full(j % stages), (j / stages) & 1);
             }
         } else if (warp == kEpiWarps + 1) {  // products
             int s = 0, acc = 0;
@@ -151,10 +149,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         s = 0;
                         ++wrap;
                     }
-                }
-                if (!ok) {  // products in flight end before the CTA leaves
-                    if (tc::elect()) tc::commit(drained);
-                    tc::bar_drain(drained, 0);
                 }
             }
         } else if (warp == kEpiWarps + 2) {  // e4m3: row scale x weight block scale of each block and column
@@ -264,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the rows of a chunk that are this CTA's: rank, rank + splits, ...
             const int slots = (32 + p.splits - 1) / p.splits;  // of a CTA, at most
 #pragma unroll 1
-            for (int c = 0; c * 32 < t.rows; ++c) {
+            for (int c = 0; ok && c * 32 < t.rows; ++c) {
                 const int rows = min(32, t.rows - c * 32), b = use & 1;
                 const int own = SPLIT ? (rows + p.splits - 1 - rank) / p.splits : rows;  // this CTA's
                 const float* box = staging + (SPLIT ? b * (kInbox / 8) : 0);
@@ -307,21 +301,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (SPLIT) {
                     ok = tc::bar_wait<tc::kCluster>(inbox_full(b), (use / 2) & 1, stop) && ok;
                     ok = epi_sync_and(ok);
+                    if (!ok) break;  // an inbox that was not filled is not armed again
                 } else {
                     epi_sync();
                 }
-                if (ok)
-                    emit_chunk(p, t, subs, bias, warp, own, t.row + c * 32 + (SPLIT ? rank + warp * p.splits : warp),
-                               SPLIT ? p.splits : 1, [&](int i, int s) {
-                                   const float* from = box + i * width + s * 128 + lane * 4;
-                                   float4 a = *reinterpret_cast<const float4*>(from);
-                                   if (SPLIT)
-                                       for (int q = 1; q < p.splits; ++q) {
-                                           const float4 w = *reinterpret_cast<const float4*>(from + q * slots * width);
-                                           a = make_float4(a.x + w.x, a.y + w.y, a.z + w.z, a.w + w.w);
-                                       }
-                                   return a;
-                               });
+                emit_chunk(p, t, subs, bias, warp, own, t.row + c * 32 + (SPLIT ? rank + warp * p.splits : warp),
+                           SPLIT ? p.splits : 1, [&](int i, int s) {
+                               const float* from = box + i * width + s * 128 + lane * 4;
+                               float4 a = *reinterpret_cast<const float4*>(from);
+                               if (SPLIT)
+                                   for (int q = 1; q < p.splits; ++q) {
+                                       const float4 w = *reinterpret_cast<const float4*>(from + q * slots * width);
+                                       a = make_float4(a.x + w.x, a.y + w.y, a.z + w.z, a.w + w.w);
+                                   }
+                               return a;
+                           });
                 if (SPLIT) {
                     epi_sync();
                     if (threadIdx.x < p.splits)
@@ -333,7 +327,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
     __syncthreads();
-    if (SPLIT) tc::cluster_sync();  // no CTA leaves while another may push into its inbox
+    // A wait gave up: copies and products in flight end before the CTA leaves.
+    // (Otherwise the epilogue has waited for them all.)
+    if (*stop) {
+        const long long t0 = clock64();
+        if (warp == kEpiWarps) {
+            for (int j = max(loads - stages, 0); j < loads; ++j) tc::bar_drain(full(j % stages), (j / stages) & 1, t0);
+        } else if (warp == kEpiWarps + 1) {
+            if (tc::elect()) tc::commit(drained);
+            tc::bar_drain(drained, 0, t0);
+        }
+        __syncwarp();
+    }
+    if (SPLIT) {
+        tc::cluster_sync();  // no CTA leaves while another may push into its inbox
+        // pushes issued before that into an inbox that nobody waits for any more
+        if (*stop) tc::nap(tc::kPushCycles);
+        __syncwarp();
+    }
     if (threadIdx.x == 0 && *stop) set_error(p.err, EP_DEVERR_TIMEOUT);
     if (warp == kEpiWarps + 1) tc::tmem_free(tmem, p.cols);
 }
@@ -470,16 +481,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     constexpr int kElems = F8 ? 128 : 64;
     Cursor cur;
     Tile t;
+    int loads = 0;  // that the loads warp has issued
 
     if (warp >= kEpiWarps) {
         tc::fewer_registers<kPairOtherRegs>();
         if (warp == kEpiWarps) {  // loads, each CTA its halves
-            int i = 0, s = 0;
+            int s = 0;
             uint32_t wrap = 0;
             bool ok = true;
             for (int id = first; ok && find_tile(p, cur, id, t); id += step) {
                 const int ch = p.parts == 2 ? t.n * 128 : t.n * 256 + rank * 128, part = p.parts == 2 ? rank : 0;
-                for (int k = 0; k < p.kblocks; ++k, ++i) {
+                for (int k = 0; k < p.kblocks; ++k, ++loads) {
                     if (wrap > 0) ok = __all_sync(FULL, tc::bar_wait(empty(s), (wrap - 1) & 1, stop));
                     if (!ok) break;
                     if (tc::elect()) {
@@ -494,9 +506,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         ++wrap;
                     }
                 }
-                if (!ok && lane == 0 && rank == 0)  // the pair's copies in flight land before it leaves
-                    for (int j = i > kPairStages ? i - kPairStages : 0; j < i; ++j)
-                        tc::bar_drain(full(j % kPairStages), (j / kPairStages) & 1);
             }
         } else if (warp == kEpiWarps + 1) {  // products, by the leader
             if (rank == 0) {
@@ -531,10 +540,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             s = 0;
                             ++wrap;
                         }
-                    }
-                    if (!ok) {  // products in flight end before the pair leaves
-                        if (tc::elect()) tc::pair_commit(drained);
-                        tc::bar_drain(drained, 0);
                     }
                 }
             }
@@ -720,6 +725,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
     __syncthreads();
+    // A wait gave up: the pair's copies and products in flight end before it
+    // leaves. The leader's barriers count both CTAs' copies, and a leader that no
+    // wait stopped has seen them all land.
+    if (*stop && rank == 0) {
+        const long long t0 = clock64();
+        if (warp == kEpiWarps) {
+            for (int j = max(loads - kPairStages, 0); j < loads; ++j)
+                tc::bar_drain(full(j % kPairStages), (j / kPairStages) & 1, t0);
+        } else if (warp == kEpiWarps + 1) {
+            if (tc::elect()) tc::pair_commit(drained);
+            tc::bar_drain(drained, 0, t0);
+        }
+        __syncwarp();
+    }
     tc::cluster_sync();
     if (threadIdx.x == 0 && *stop) set_error(p.err, EP_DEVERR_TIMEOUT);
     if (warp == kEpiWarps + 1) tc::pair_tmem_free(tmem, 512);

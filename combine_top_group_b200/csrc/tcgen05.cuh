@@ -85,11 +85,17 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
     }
     return true;
 }
-// The same without the stop flag, for draining what a stopped CTA has in flight.
-__device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity) {
-    const long long t0 = clock64();
+// The same without the stop flag, for draining what a stopped CTA has in
+// flight; several drains share the limit from t0 on.
+__device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity, long long t0) {
     while (!bar_try(bar, parity))
         if (clock64() - t0 > kWaitLimitCycles) return;
+}
+// About 1 ms, a thousand times what a store into another CTA's shared memory takes.
+constexpr long long kPushCycles = 2000000ll;
+__device__ __forceinline__ void nap(long long cycles) {
+    const long long t0 = clock64();
+    while (clock64() - t0 < cycles) __nanosleep(1000);
 }
 
 // ---- TMA ---------------------------------------------------------------------

@@ -55,3 +55,26 @@ def test_inboxes_are_handed_over_at_the_clusters_scope():
     ptx = code("tcgen05.cuh")
     assert "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64" in ptx
     assert "mbarrier.arrive.release.cluster.shared::cluster.b64" in ptx
+
+
+@pytest.mark.parametrize("name", ["linear_kernel", "linear_pair_kernel"])
+def test_a_stopped_cta_drains_whatever_stopped_it(name):
+    """A wait that gives up may be any warp's. So what is in flight is drained
+    after the barrier of the whole CTA, where the stop flag is final, and not
+    by the one warp that saw its own wait fail."""
+    k = kernels()[name]
+    end = k.rindex("__syncthreads();")
+    assert "bar_drain" not in k[:end]
+    after = k[end:]
+    assert re.match(r"__syncthreads\(\); if \(\*stop( && rank == 0)?\) \{", after)
+    assert re.search(r"bar_drain\(full\(", after) and re.search(r"commit\(drained\); tc::bar_drain\(drained", after)
+    assert after.index("bar_drain") < after.index("cluster_sync") < after.index("tmem_free")
+
+
+def test_an_unfilled_inbox_is_not_armed_again():
+    """Arming an mbarrier whose phase is incomplete is undefined: the epilogue
+    leaves its loop as soon as an inbox wait has given up."""
+    k = kernels()["linear_kernel"]
+    wait = k.index("bar_wait<tc::kCluster>(inbox_full")
+    assert re.match(r"[^;]*; ok = epi_sync_and\(ok\); if \(!ok\) break;", k[wait:])
+    assert k.count("bar_expect(inbox_full") == 1
