@@ -110,6 +110,9 @@ struct Tile {
     int rows;              // valid rows, at most bn
 };
 
+// Tiles of bn rows that `count` rows take; count + bn - 1 may not fit 31 bits.
+__device__ __forceinline__ int row_tiles(int count, int bn) { return count > 0 ? (count - 1) / bn + 1 : 0; }
+
 __device__ __forceinline__ bool find_tile(const LinearParams& p, Cursor& c, int id, Tile& t) {
     const int lane = threadIdx.x & 31;
     while (id >= c.base + c.total) {
@@ -119,7 +122,7 @@ __device__ __forceinline__ bool find_tile(const LinearParams& p, Cursor& c, int 
         c.start = 0;
         c.count = 0;
         if (c.g0 + lane < p.G) group_rows(p, c.g0 + lane, c.start, c.count);
-        int64_t incl = (int64_t)((c.count + p.bn - 1) / p.bn) * p.nt;
+        int64_t incl = (int64_t)row_tiles(c.count, p.bn) * p.nt;
         c.mine = (int)incl;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -140,7 +143,7 @@ __device__ __forceinline__ bool find_tile(const LinearParams& p, Cursor& c, int 
     const int at = in_window - (__shfl_sync(FULL, c.incl, src) - __shfl_sync(FULL, c.mine, src));
     const int count = __shfl_sync(FULL, c.count, src);
     const int64_t start = __shfl_sync(FULL, c.start, src);
-    const int tt = (count + p.bn - 1) / p.bn;
+    const int tt = row_tiles(count, p.bn);
     t.group = c.g0 + src;
     t.n = at / tt;
     const int r = (at - t.n * tt) * p.bn;

@@ -490,6 +490,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t wrap = 0;
             bool ok = true;
             for (int id = first; ok && find_tile(p, cur, id, t); id += step) {
+                // the CTA's half of the tile; from row_limit on it is zeros
+                const int row = (int)min(t.row + rank * 128, p.row_limit);
                 const int ch = p.parts == 2 ? t.n * 128 : t.n * 256 + rank * 128, part = p.parts == 2 ? rank : 0;
                 for (int k = 0; k < p.kblocks; ++k, ++loads) {
                     if (wrap > 0) ok = __all_sync(FULL, tc::bar_wait(empty(s), (wrap - 1) & 1, stop));
@@ -497,7 +499,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (tc::elect()) {
                         const uint32_t at = ring + s * kPairStage, bar = tc::peer_smem(full(s), 0);
                         if (rank == 0) tc::bar_expect(full(s), 2 * kPairStage);
-                        tc::pair_tma_2d(at, &map_x, bar, k * kElems, (int)t.row + rank * 128);
+                        tc::pair_tma_2d(at, &map_x, bar, k * kElems, row);
                         tc::pair_tma_4d(at + kSub, &map_w, bar, k * kElems, ch, part, t.group / p.R);
                     }
                     __syncwarp();

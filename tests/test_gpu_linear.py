@@ -495,3 +495,19 @@ def test_moe_block(ep, fp8):
     assert torch.equal(counts.long(), b64[1]) and torch.equal(counts[0], lay["num_tokens_per_expert"])
     assert abs(loss[0].double() - b64[0]) <= b64[0] * 2.0 ** -17
     assert dl.isfinite().all()
+
+
+def test_rows_up_to_2_31(ep):
+    """The most rows that a call takes: the tile count of 2^31 - 1 rows needs
+    more than 31 bits on its way."""
+    rows, cin = 2 ** 31 - 1, 8
+    x = torch.zeros(rows, cin, dtype=BF, device=DEV)
+    x[-3:] = torch.randn(3, cin, generator=gen(1), device=DEV).to(BF)
+    s = operands(1, "bf16", 1, 1, cin, 1, 0, False, False)
+    o = torch.full((rows, 1), 7.0, dtype=BF, device=DEV)
+    buf = buffer(ep, 1, 1, 1, 1)
+    ep.ep_linear(buf, x, s["w"], o)
+    assert ep.ep_check_errors(buf) == 0
+    s["x"] = x
+    check(s, o, None, rows - 3, 3, 0, 0, 1, "bf16")
+    assert not o[:-3].any()
