@@ -49,21 +49,22 @@ struct LinearParams {
 // Rows [start, start + count) of group g; none, and an error bit, where they
 // leave [0, row_limit).
 __device__ __forceinline__ void group_rows(const LinearParams& p, int g, int64_t& start, int& count) {
+    int64_t n;
     if (p.off) {
         start = p.off[g];
-        count = p.off[g + 1] - (int)start;
+        n = p.off[g + 1] - start;
     } else if (p.cnt) {
         start = (int64_t)g * p.region;
-        count = min(p.cnt[(int64_t)(g % p.R) * (p.G / p.R) + g / p.R], (int)p.region);
+        n = min((int64_t)p.cnt[(int64_t)(g % p.R) * (p.G / p.R) + g / p.R], p.region);
     } else {
         start = 0;
-        count = (int)p.rows;
+        n = p.rows;
     }
-    if (count > 0 && (start < 0 || start + count > p.row_limit)) {
+    if (n > 0 && (start < 0 || start + n > p.row_limit)) {
         set_error(p.err, EP_DEVERR_ROW_BOUNDS);
-        count = 0;
+        n = 0;
     }
-    count = max(count, 0);
+    count = (int)max(n, (int64_t)0);
 }
 
 __device__ __forceinline__ float activate(int act, float z) {

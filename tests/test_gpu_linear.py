@@ -511,3 +511,21 @@ def test_rows_up_to_2_31(ep):
     s["x"] = x
     check(s, o, None, rows - 3, 3, 0, 0, 1, "bf16")
     assert not o[:-3].any()
+
+
+def test_offsets_too_far_apart(ep):
+    """An expert whose offsets are more than 2^31 apart is reported too."""
+    T, E, cin, cout = 30, 4, 128, 256
+    buf = buffer(ep, 1, T, E, 1)
+    idx = (torch.arange(T, device=DEV, dtype=torch.int32) * E // T).view(T, 1).contiguous()
+    ep.ep_get_layout(buf, T, topk_idx=idx, topk_w=torch.ones(T, 1, device=DEV))
+    off = ep.ep_buffer_layout(buf, T)["expert_off"]
+    off[3], off[4] = -2, 2 ** 31 - 1
+    now = off.tolist()
+    s = operands(3, "bf16", T, E, cin, cout, 0, False, False)
+    o, _ = outputs(T, cout, "bf16")
+    ep.ep_expert_linear(buf, T, s["x"], s["w"], o)
+    assert ep.ep_check_errors(buf) == ep.EP_DEVERR_ROW_BOUNDS
+    for g in range(2):
+        check(s, o, None, now[g], now[g + 1] - now[g], g, 0, cout, "bf16")
+    untouched(o, None, slice(now[2], None))
