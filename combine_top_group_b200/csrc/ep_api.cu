@@ -390,7 +390,8 @@ ep_status_t ep_get_layout(ep_buffer_t* b, int T, const float* d_logits, const in
 
 ep_status_t ep_dispatch(ep_buffer_t* b, int T, const void* d_x, void* stream) {
     if (ep_status_t st = check_single(b)) return st;
-    if (T != b->last_T) return fail(EP_ERR_INVALID, "T=%d does not match the last ep_get_layout (T=%d)", T, b->last_T);
+    if (T < 0 || T != b->last_T)
+        return fail(EP_ERR_INVALID, "T=%d does not match the last ep_get_layout (T=%d)", T, b->last_T);
     if (T > 0 && !d_x) return fail(EP_ERR_INVALID, "d_x is NULL");
     if ((uintptr_t)d_x % 32 != 0) return fail(EP_ERR_INVALID, "d_x must be 32-byte aligned");
     cudaError_t e = ep::launch_dispatch(*b, T, d_x, static_cast<cudaStream_t>(stream));
@@ -400,7 +401,8 @@ ep_status_t ep_dispatch(ep_buffer_t* b, int T, const void* d_x, void* stream) {
 
 ep_status_t ep_combine(ep_buffer_t* b, int T, const void* d_y, const float* d_y_scale, void* d_out, void* stream) {
     if (ep_status_t st = check_single(b)) return st;
-    if (T != b->last_T) return fail(EP_ERR_INVALID, "T=%d does not match the last ep_get_layout (T=%d)", T, b->last_T);
+    if (T < 0 || T != b->last_T)
+        return fail(EP_ERR_INVALID, "T=%d does not match the last ep_get_layout (T=%d)", T, b->last_T);
     if (T > 0 && (!d_y || !d_out)) return fail(EP_ERR_INVALID, "d_y and d_out must be non-NULL");
     if ((uintptr_t)d_y % 32 != 0 || (uintptr_t)d_out % 32 != 0)
         return fail(EP_ERR_INVALID, "d_y and d_out must be 32-byte aligned");
@@ -432,7 +434,8 @@ ep_status_t ep_buffer_dedup(const ep_buffer_t* b, int32_t** tok_row, int32_t** r
 static ep_status_t check_dedup_call(const ep_buffer_t* b, int T) {
     if (ep_status_t st = check_buf(b)) return st;
     if (!(b->cfg.flags & EP_FLAG_DEDUP)) return fail(EP_ERR_INVALID, "buffer was created without EP_FLAG_DEDUP");
-    if (T != b->last_T) return fail(EP_ERR_INVALID, "T=%d does not match the last ep_get_layout (T=%d)", T, b->last_T);
+    if (T < 0 || T != b->last_T)
+        return fail(EP_ERR_INVALID, "T=%d does not match the last ep_get_layout (T=%d)", T, b->last_T);
     return EP_OK;
 }
 
@@ -485,7 +488,8 @@ static ep_status_t check_shard_step(const ep_buffer_t* b, int rank, int T, bool 
     if (b->shard_rank < 0) return fail(EP_ERR_INVALID, "no ep_shard_layout on this buffer yet");
     if (rank != b->shard_rank)
         return fail(EP_ERR_INVALID, "rank=%d does not match the last ep_shard_layout (rank=%d)", rank, b->shard_rank);
-    if (T != b->last_T) return fail(EP_ERR_INVALID, "T=%d does not match the last ep_shard_layout (T=%d)", T, b->last_T);
+    if (T < 0 || T != b->last_T)
+        return fail(EP_ERR_INVALID, "T=%d does not match the last ep_shard_layout (T=%d)", T, b->last_T);
     if (need_placed && !b->placed) return fail(EP_ERR_INVALID, "call ep_shard_place after ep_shard_layout first");
     return EP_OK;
 }

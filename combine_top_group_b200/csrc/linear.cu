@@ -315,7 +315,8 @@ ep_status_t ep_linear(ep_buffer_t* b, int64_t rows, const ep_linear_t* q, void* 
 ep_status_t ep_expert_linear(ep_buffer_t* b, int T, const ep_linear_t* q, void* stream) {
     using namespace ep;
     if (!b) return fail(EP_ERR_INVALID, "buffer is NULL");
-    if (T != b->last_T) return fail(EP_ERR_INVALID, "T=%d does not match the last layout (T=%d)", T, b->last_T);
+    if (T < 0 || T != b->last_T)
+        return fail(EP_ERR_INVALID, "T=%d does not match the last layout (T=%d)", T, b->last_T);
     const bool sh = (b->cfg.flags & EP_FLAG_SHARD) != 0;
     if (sh && !b->placed) return fail(EP_ERR_INVALID, "call ep_shard_place after ep_shard_layout first");
     const int64_t rows = (int64_t)b->cfg.num_ranks * T * b->cfg.topk;

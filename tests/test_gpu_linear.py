@@ -529,3 +529,21 @@ def test_offsets_too_far_apart(ep):
     for g in range(2):
         check(s, o, None, now[g], now[g + 1] - now[g], g, 0, cout, "bf16")
     untouched(o, None, slice(now[2], None))
+
+
+@pytest.mark.parametrize("flags", [0, 2, 4])
+def test_no_layout_yet(ep, flags):
+    """Before any layout every T is refused, the negative ones as well."""
+    buf = buffer(ep, 1, 8, 4, 2, flags)
+    s = operands(7, "bf16", 64, 4, 128, 64, 0, False, False)
+    o, _ = outputs(64, 64, "bf16")
+    y = torch.zeros(64, 128, dtype=BF, device=DEV)
+    calls = [lambda t: ep.ep_expert_linear(buf, t, s["x"], s["w"], o)]
+    calls += [lambda t: ep.ep_dispatch_dedup(buf, t, y), lambda t: ep.ep_permute(buf, t)] if flags == 4 else \
+        [lambda t: ep.ep_dispatch(buf, t, y), lambda t: ep.ep_combine(buf, t, y, None, y.clone())]
+    for call in calls:
+        for t in (-1, 0, 8):
+            with pytest.raises(ep.EpError) as e:
+                call(t)
+            assert e.value.status == ep.EP_ERR_INVALID
+    untouched(o, None, slice(None))
