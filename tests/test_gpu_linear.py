@@ -547,3 +547,55 @@ def test_no_layout_yet(ep, flags):
                 call(t)
             assert e.value.status == ep.EP_ERR_INVALID
     untouched(o, None, slice(None))
+
+
+def positive(seed, kind, rows, cin, cout):
+    """Operands of one sign, so that nothing cancels, rows of sizes spread over an octave."""
+    s = operands(seed, kind, rows, 1, cin, cout, 0, False, False)
+    spread = 1 + torch.rand(rows, 1, generator=gen(seed + 1), device=DEV)
+    s["w"] = s["w"].float().abs().to(s["w"].dtype)
+    s["x"] = (s["x"].float().abs() * (spread if kind == "bf16" else 1)).to(s["x"].dtype)
+    return s
+
+
+def product(s, cout):
+    x = s["x"].double()
+    if s["x_scale"] is not None:
+        x = x * s["x_scale"].double().repeat_interleave(128, 1)
+    w = ref.weight64(s["w"], s["w_scale"], cout)[0]
+    return torch.cat([x @ w[n:n + 1024].t() for n in range(0, cout, 1024)], 1)
+
+
+# rows, out_features: a cluster for each tile; one CTA for each; pairs of CTAs
+KERNELS = [(3, 512), (40, 148 * 512), (512, 2048)]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("rows,cout", KERNELS)
+def test_exactness_of_deep_sums(ep, kind, rows, cout):
+    """fp32 outputs of 7168 channels. Tensor memory cuts about 1.5e-8 of a sum
+    with each step of 16 channels. bf16: 32 steps at a time (4.8e-7 in the mean,
+    under 1e-6 with their spread), then 14 parts and at most 8 of a cluster are
+    added in fp32 (2^-24 each at most, of either sign: under 1e-6). All 448 steps
+    in one go would cut 6.7e-6. e4m3: 56 blocks of 4 steps, each scaled and added
+    in fp32, with 72 roundings of 2^-24 at most."""
+    s = positive(1, kind, rows, 7168, cout)
+    o = torch.empty(rows, cout, device=DEV)
+    ep.ep_linear(buffer(ep, 1, 1, 1, 1), s["x"], s["w"], o, x_scale=s["x_scale"], w_scale=s["w_scale"])
+    y = product(s, cout)
+    ref.within(o, y, y * (2e-6 if kind == "bf16" else 72 * 2.0 ** -24), "out")
+
+
+@pytest.mark.parametrize("rows,cout", [(3, 128), (300, 256)])
+def test_bf16_outputs_of_the_deepest_sums(ep, rows, cout):
+    """2^19 channels, bf16 out: half a step of the value itself, and what the
+    sum may lose: 512 steps in tensor memory (7.7e-6), 64 parts added in fp32
+    (3.8e-6). In one go it would be cut by 5e-4, and every tenth output would be
+    rounded the wrong way."""
+    cin = 2 ** 19
+    s = positive(1, "bf16", rows, cin, cout)
+    o = torch.empty(rows, cout, dtype=BF, device=DEV)
+    ep.ep_linear(buffer(ep, 1, 1, 1, 1), s["x"], s["w"], o)
+    y = product(s, cout)
+    half = torch.ldexp(torch.ones_like(y), torch.frexp(y).exponent - 9)
+    ref.within(o, y, half + y * 2e-5, "out")
