@@ -489,11 +489,17 @@ ep_status_t check(int64_t N, int E, int K, int S, const int32_t* off) {
 template <int LT, int VPL, bool VEC>
 void launch_as(const BalanceParams& p, bool backward, cudaStream_t s) {
     const bool soft = p.score == EP_SCORE_SOFTMAX;
-    const int ring = kWarps * Rows<VPL, VEC>::kWarpBytes, smem = ring + (backward ? 0 : (kWarps + 1) * p.E * 4);
+    constexpr int ring = kWarps * Rows<VPL, VEC>::kWarpBytes;
+    // The kernel's limit is what the most experts that it serves need, in every
+    // call: another host thread's call, of other experts, may come between this
+    // one's limit and its launch.
+    constexpr int most = ring + (kWarps + 1) * (LT ? LT : 32) * VPL * 4;
+    static_assert(most <= 227 * 1024, "shared memory");
+    const int smem = ring + (backward ? 0 : (kWarps + 1) * p.E * 4);
     const auto kernel =
         backward ? (soft ? balance_backward_kernel<LT, VPL, VEC, true> : balance_backward_kernel<LT, VPL, VEC, false>)
                  : (soft ? balance_partial_kernel<LT, VPL, VEC, true> : balance_partial_kernel<LT, VPL, VEC, false>);
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e == cudaSuccess) kernel<<<(unsigned)p.nchunks, kWarps * 32, smem, s>>>(p);
 }
 

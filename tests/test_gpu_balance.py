@@ -253,3 +253,37 @@ def test_graph_and_streams(ep):
     for s, w in ((a, want[0]), (b, want[1])):
         for x in names:
             assert torch.equal(s[x], w[x]), x
+
+
+def test_two_host_threads(ep):
+    """Two host threads call the loss at once, each on arrays of its own and
+    with a number of experts of its own that the same kernel serves. (The C
+    function itself: it runs without the interpreter's lock.)"""
+    import sys
+    import threading
+    got, gate = {}, threading.Barrier(2)
+
+    def calls(e, st):
+        z, idx = case(e, 64, e, 4)
+        loss, counts = torch.empty(1, device=DEV), torch.empty(1, e, dtype=torch.int32, device=DEV)
+        ws = torch.empty(ep.ep_balance_loss_workspace_bytes(64, e), dtype=torch.uint8, device=DEV)
+        err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        a = (64, e, 4, 0, z.data_ptr(), idx.data_ptr(), 1, None, 1.0, loss.data_ptr(), counts.data_ptr(), None,
+             ws.data_ptr(), ws.numel(), err.data_ptr(), st.cuda_stream)
+        torch.cuda.synchronize()
+        gate.wait(60)
+        failed = sum(ep._lib.ep_balance_loss(*a) != 0 for _ in range(10000))
+        st.synchronize()
+        l64, c64, _ = ref.balance(z.double(), idx, 0, 1.0, [0, 64])
+        got[e] = failed, torch.equal(counts.long(), c64), abs(loss[0].double() - l64).item() <= l64.item() * REL, err.item()
+    threads = [threading.Thread(target=calls, args=(e, torch.cuda.Stream())) for e in (68, 128)]
+    every = sys.getswitchinterval()
+    sys.setswitchinterval(1e-6)
+    try:
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    finally:
+        sys.setswitchinterval(every)
+    assert got == {68: (0, True, True, 0), 128: (0, True, True, 0)}
