@@ -11,6 +11,7 @@
 #include <new>
 
 #include "ep.h"
+#include "fail.h"
 #include "internal.h"
 
 namespace {

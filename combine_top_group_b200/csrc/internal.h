@@ -58,8 +58,6 @@ namespace ep {
 
 // Sets the message ep_last_error_message() returns on this host thread.
 void set_last_error(const char* msg);
-// The same with a format; returns st.
-ep_status_t fail(ep_status_t st, const char* fmt, ...);
 
 // Layout grid cap (CTAs = chunks) and the control words at the head of the
 // layout scratch (two barrier counters, zero between launches).

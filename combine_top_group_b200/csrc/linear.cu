@@ -28,6 +28,7 @@
 #include <atomic>
 
 #include "ep.h"
+#include "fail.h"
 #include "internal.h"
 #include "linear.cuh"
 

@@ -11,6 +11,7 @@
 
 #include "common.cuh"
 #include "ep.h"
+#include "fail.h"
 #include "internal.h"
 
 namespace ep {

@@ -133,3 +133,15 @@ def test_source_hash_ignores_comments_not_code(tmp_path, monkeypatch):
     assert metrics.source_hash("combine") == base
     (tmp_path / "combine.cu").write_text(src.replace("kTmaStages = 4", "kTmaStages = 3", 1))
     assert metrics.source_hash("combine") != base
+
+
+def test_stored_traffic_is_of_the_present_kernels():
+    """Each stored figure was captured from the code that is there now, so the
+    bench reports it. (After a change of a kernel it is captured anew; a change
+    that no kernel sees belongs in a file that the hash does not cover.)"""
+    with open(metrics.TRAFFIC_FILE) as f:
+        data = json.load(f)
+    assert data
+    for wname, ent in data.items():
+        for kern, k in ent.items():
+            assert metrics.stored_traffic(kern, wname) == k["dram_bytes_per_launch"], (wname, kern)
