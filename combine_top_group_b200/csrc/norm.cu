@@ -381,34 +381,30 @@ struct NormBwdParams {
     const uint16_t* dy;
     const uint16_t* dh;
     uint16_t* dx;
-    float* part;  // [CTAs * rows per CTA][H]
+    float* part;  // [CTAs][H]
 };
 
-// Each row slot (a CTA's rows-per-CTA of them) walks rows slot, slot + slots,
+// Rows over 16384 channels, one at a time per CTA: CTA b takes rows b, b + CTAs,
 // ... and keeps its dgamma sums in registers until the end.
 template <int VPT>
-__global__ void __launch_bounds__(1024) rmsnorm_bwd_kernel(NormBwdParams p) {
+__global__ void __launch_bounds__(1024, 1) rmsnorm_bwd_kernel(NormBwdParams p) {
     __shared__ float red[2][32];
-    const int rpc = blockDim.x / p.tpr;
-    const int sub = threadIdx.x / p.tpr, t = threadIdx.x - sub * p.tpr;
-    const int64_t slot = (int64_t)blockIdx.x * rpc + sub, slots = (int64_t)gridDim.x * rpc;
+    const int t = threadIdx.x;
     float dg[VPT][kVec];
 #pragma unroll
     for (int j = 0; j < VPT; ++j)
 #pragma unroll
         for (int i = 0; i < kVec; ++i) dg[j][i] = 0.f;
     int flip = 0;
-    for (int64_t row0 = (int64_t)blockIdx.x * rpc; row0 < p.N; row0 += slots, flip ^= 1) {
-        const int64_t row = row0 + sub;
-        const bool live = row < p.N;
-        const int64_t base = live ? row * p.H : 0;
-        const float rstd = live ? p.rstd[row] : 0.f;
+    for (int64_t row = blockIdx.x; row < p.N; row += gridDim.x, flip ^= 1) {
+        const int64_t base = row * p.H;
+        const float rstd = p.rstd[row];
         float n[VPT][kVec], dt[VPT][kVec];
         float dot = 0.f;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int k = t + j * p.tpr;
-            if (live && k < p.nv) {
+            if (k < p.nv) {
                 const u32x8 a = ld256_stream(p.h + base + k * kVec), b = ld256_stream(p.dy + base + k * kVec);
                 float g[kVec];
                 load_gamma(p.gamma, p.gamma_fp32, k * kVec, g);
@@ -431,7 +427,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_bwd_kernel(NormBwdParams p) {
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int k = t + j * p.tpr;
-            if (live && k < p.nv) {
+            if (k < p.nv) {
                 u32x8 c;
                 if (p.dh) c = ld256_stream(p.dh + base + k * kVec);
 #pragma unroll
@@ -452,7 +448,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_bwd_kernel(NormBwdParams p) {
     for (int j = 0; j < VPT; ++j) {
         const int k = t + j * p.tpr;
         if (k < p.nv) {
-            float4* o = reinterpret_cast<float4*>(p.part + slot * p.H + k * kVec);
+            float4* o = reinterpret_cast<float4*>(p.part + (int64_t)blockIdx.x * p.H + k * kVec);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 o[i] = make_float4(dg[j][4 * i], dg[j][4 * i + 1], dg[j][4 * i + 2], dg[j][4 * i + 3]);
@@ -460,7 +456,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_bwd_kernel(NormBwdParams p) {
     }
 }
 
-// rmsnorm_bwd_kernel on a stream of rows. At the end a CTA adds its rows-per-CTA
+// The gradient on a stream of rows. At the end a CTA adds its rows-per-CTA
 // dgamma sums through shared memory, in row order, and writes one partial row.
 template <int VPT, bool DH>
 __global__ void __launch_bounds__(512) rmsnorm_bwd_stream_kernel(NormBwdParams p) {
@@ -611,46 +607,40 @@ constexpr int64_t kMaxSlots = 592;
 // A stream kernel runs from this many row groups on.
 constexpr int64_t kStreamRows = 592;
 
-int64_t bwd_slots(int64_t N, int tpr) {
-    const int rpc = rows_per_cta(tpr);
-    const int64_t rows = (N + rpc - 1) / rpc * rpc;
-    const int64_t most = kMaxSlots / rpc * rpc;
-    return rows < most ? rows : most;
-}
+int64_t bwd_slots(int64_t N) { return N < kMaxSlots ? N : kMaxSlots; }
 
 constexpr int kMaxStreamSmem = 226 * 1024;  // beside the reduction's static 256 bytes
 
-// CTAs that the current device holds at once (per SM, on its SMs); 0 on an
-// error. Sets the kernel's shared-memory limit. The host thread's last counts
+// CTAs of a stream kernel that the current device holds at once (per SM, on its
+// SMs). Sets the kernel's shared-memory limit. The host thread's last counts
 // are kept, since asking takes longer than the launch; the limit is set by every
-// call, always to the same value: a reset of the device forgets it.
-int resident(const void* kernel, int threads, int smem, int* per, int* sms) {
+// call, always to the same value: a reset of the device forgets it. On an error
+// the call fails: another kernel in its place would add up in another order, and
+// the same call would not give the same bits.
+ep_status_t resident(const void* kernel, int threads, int smem, int* per, int* sms) {
     struct Known {
         const void* kernel;
         int threads, smem, dev, per, sms;
     };
     static thread_local Known known{};
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxStreamSmem) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    if (known.kernel != kernel || known.threads != threads || known.smem != smem || known.dev != dev) {
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxStreamSmem);
+    if (e == cudaSuccess &&
+        (known.kernel != kernel || known.threads != threads || known.smem != smem || known.dev != dev)) {
         known.kernel = nullptr;
-        if (cudaDeviceGetAttribute(&known.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&known.per, kernel, threads, smem) != cudaSuccess) {
-            cudaGetLastError();
-            return 0;
-        }
-        known.kernel = kernel;
-        known.threads = threads;
-        known.smem = smem;
-        known.dev = dev;
+        e = cudaDeviceGetAttribute(&known.sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&known.per, kernel, threads, smem);
+        if (e == cudaSuccess) known = {kernel, threads, smem, dev, known.per, known.sms};
+    }
+    if (e == cudaSuccess && known.per < 1) e = cudaErrorInvalidConfiguration;
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return fail(EP_ERR_CUDA, "resident CTAs of the norm's kernel: %s", cudaGetErrorString(e));
     }
     *per = known.per;
     *sms = known.sms;
-    return *per * *sms;
+    return EP_OK;
 }
 
 ep_status_t check_shape(int64_t N, int H, int gamma_type) {
@@ -721,16 +711,15 @@ ep_status_t ep_rmsnorm(int64_t N, int H, const void* d_x, const void* d_residual
         const int64_t groups = (N + rps - 1) / rps;
         if (groups >= kStreamRows) {
             int per = 0, sms = 0;
-            int ctas = resident((const void*)kernel, threads, smem, &per, &sms);
+            if (ep_status_t st = resident((const void*)kernel, threads, smem, &per, &sms)) return st;
+            int ctas = per * sms;
             // HBM bounds a stream with a residual, and one CTA per SM then reads
             // and writes faster than two (32768 x 7168: 6.44 against 5.57 TB/s);
             // instructions bound one without (153 against 185 us), and the
             // reduction's latency a few rows per SM.
             if (per > 1 && ps.res && groups >= 16 * sms) ctas = sms;
-            if (ctas > 0) {
-                kernel<<<(unsigned)(groups < ctas ? groups : ctas), threads, smem, s>>>(ps);
-                return launched("rmsnorm");
-            }
+            kernel<<<(unsigned)(groups < ctas ? groups : ctas), threads, smem, s>>>(ps);
+            return launched("rmsnorm");
         }
     }
     const int rpc = rows_per_cta(p.tpr);
@@ -745,9 +734,7 @@ ep_status_t ep_rmsnorm_backward_workspace_bytes(int64_t N, int H, size_t* bytes)
     using namespace ep;
     if (ep_status_t st = check_shape(N, H, EP_DTYPE_BF16)) return st;
     if (!bytes) return fail(EP_ERR_INVALID, "bytes is NULL");
-    int nv, tpr, vpt;
-    shape_of(H, &nv, &tpr, &vpt);
-    *bytes = (size_t)(N > 0 ? bwd_slots(N, tpr) : 1) * H * sizeof(float);
+    *bytes = (size_t)(N > 0 ? bwd_slots(N) : 1) * H * sizeof(float);
     set_last_error("");
     return EP_OK;
 }
@@ -802,22 +789,19 @@ ep_status_t ep_rmsnorm_backward(int64_t N, int H, const void* d_h, const float* 
                       : (ps.dh ? rmsnorm_bwd_stream_kernel<2, true> : rmsnorm_bwd_stream_kernel<2, false>);
         const int64_t groups = (N + rps - 1) / rps;
         int per = 0, sms = 0;
-        int64_t ctas = resident((const void*)kernel, threads, smem, &per, &sms);
-        const int64_t rows = bwd_slots(N, p.tpr);  // what the workspace holds
+        if (ep_status_t st = resident((const void*)kernel, threads, smem, &per, &sms)) return st;
+        int64_t ctas = (int64_t)per * sms;
+        const int64_t rows = bwd_slots(N);  // what the workspace holds
         if (ctas > rows) ctas = rows;
         if (groups < ctas) ctas = groups;
-        if (ctas > 0) {
-            kernel<<<(unsigned)ctas, threads, smem, s>>>(ps);
-            if (ep_status_t st = launched("rmsnorm backward")) return st;
-            dgamma_kernel<<<H / 32, 1024, 0, s>>>(p.part, (int)ctas, H, d_dgamma);
-            return launched("dgamma");
-        }
+        kernel<<<(unsigned)ctas, threads, smem, s>>>(ps);
+        if (ep_status_t st = launched("rmsnorm backward")) return st;
+        dgamma_kernel<<<H / 32, 1024, 0, s>>>(p.part, (int)ctas, H, d_dgamma);
+        return launched("dgamma");
     }
-    const int rpc = rows_per_cta(p.tpr);
-    const int slots = (int)bwd_slots(N, p.tpr);
-    if (vpt == 1) rmsnorm_bwd_kernel<1><<<slots / rpc, p.tpr * rpc, 0, s>>>(p);
-    else if (vpt == 2) rmsnorm_bwd_kernel<2><<<slots / rpc, p.tpr * rpc, 0, s>>>(p);
-    else rmsnorm_bwd_kernel<4><<<slots / rpc, p.tpr * rpc, 0, s>>>(p);
+    const int slots = (int)bwd_slots(N);
+    if (vpt == 2) rmsnorm_bwd_kernel<2><<<slots, p.tpr, 0, s>>>(p);
+    else rmsnorm_bwd_kernel<4><<<slots, p.tpr, 0, s>>>(p);
     if (ep_status_t st = launched("rmsnorm backward")) return st;
     dgamma_kernel<<<H / 32, 1024, 0, s>>>(p.part, slots, H, d_dgamma);
     return launched("dgamma");

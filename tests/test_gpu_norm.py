@@ -276,3 +276,10 @@ def test_graph_and_streams(ep):
     for s, w in ((a, want[0]), (b, want[1])):
         for k, t in w.items():
             assert torch.equal(s[k], t), k
+
+
+@pytest.mark.parametrize("n,h", [(700, 16512), (1300, 32896), (601, 65536)])
+def test_backward_of_many_long_rows(ep, n, h):
+    """Rows too long for the streams, several to a CTA."""
+    test_backward(ep, n, h, F32, True)
+    test_backward(ep, n, h, BF, False)

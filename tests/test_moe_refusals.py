@@ -97,3 +97,14 @@ def test_host_tensors_are_refused():
                            torch.zeros(1, dtype=torch.int32))
     with pytest.raises(ep.EpError):
         ep.ep_balance_loss_backward(z, torch.zeros(1, 16, dtype=torch.int32), 2, 0, 1.0, z.clone())
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are made up: nothing may be launched on them")
+def test_norm_without_a_device():
+    """Where the device cannot be asked what it holds at once, the call fails
+    there. (It does not fall back to a kernel that adds up in another order.)"""
+    big = dict(N=100000, H=256)
+    assert status("ep_rmsnorm", *{**NORM, **big}.values()) == ep.EP_ERR_CUDA
+    assert "resident CTAs" in ep.ep_last_error_message()
+    assert status("ep_rmsnorm_backward", *{**BACK, **big}.values()) == ep.EP_ERR_CUDA
+    assert "resident CTAs" in ep.ep_last_error_message()
