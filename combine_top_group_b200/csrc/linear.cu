@@ -13,14 +13,15 @@
 //  - e4m3: each block of 128 channels is summed on its own in tensor memory
 //    and leaves it times its scales (row scale x weight block scale, fp32)
 //    into fp32 registers, since the scales differ from block to block.
-//  - bf16: the whole sum up to 8192 channels, then in parts of 8192, or for
-//    fp32 and e4m3 outputs every 8 blocks of 64 channels, leaves tensor memory
-//    the same way. Sums there lose about 1.5e-8 of their size with each step of
-//    16 channels (they are cut, not rounded: 7.7e-6 over 8192 channels). That
-//    is nothing beside a bf16 output's 2^-9, but 2^20 channels in one go would
-//    lose 1e-3, half of that; 32 steps keep it below the roundings of an fp32
-//    sum of that length (4.8e-7 measured for 512 to 7168 channels), at the price
-//    of 8 to 20% of the time.
+//  - bf16: the whole sum leaves tensor memory the same way; beyond 8192 channels
+//    parts of 2048 do, and for fp32 and e4m3 outputs every 8 blocks of 64. Sums
+//    there are cut, not rounded: operands of one sign lose 2.5e-8 (32 steps of
+//    16 channels) to 6e-8 (512 steps) of the sum with each step. So bf16 outputs
+//    are off by at most 3.2e-5 before their own rounding by up to 2^-9 or 2^-8
+//    (in one go 2^19 channels lost 3.6e-4 even split over a cluster), fp32 and
+//    e4m3 outputs by 8e-7, about what roundings of an fp32 sum of that length
+//    come to. The price is 7% of the time beyond 8192 channels, and 8 to 20% for
+//    fp32 and e4m3 outputs.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -114,8 +115,6 @@ LinearParams params_of(const ep_linear_t& q) {
 }
 
 constexpr int kMaxSplits = 8;
-// Blocks of 64 channels that a bf16 output sums in tensor memory at a time.
-constexpr int kMostFlush = 128;
 
 // Clusters of n CTAs, one CTA per SM, that device b can hold at once: fewer
 // than SMs / n, since a cluster stays within a GPC (15 of 8, not 18).
@@ -234,7 +233,7 @@ ep_status_t launch_on_device(const ep_buffer& b, LinearParams p, int64_t x_rows,
     const int size = f8 ? 1 : 2;
     p.kblocks = f8 ? p.K / 128 : (p.K + 63) / 64;
     p.vec = p.N % 4 == 0;
-    p.flush = f8 ? 1 : p.out_type == EP_DTYPE_BF16 ? kMostFlush : 8;
+    p.flush = f8 ? 1 : p.out_type != EP_DTYPE_BF16 ? 8 : p.kblocks <= 128 ? p.kblocks : 32;
     if (p.flush > p.kblocks) p.flush = p.kblocks;
     const Shape c = shape_of(b, p, avg, most);
     const bool pair = c.pair;

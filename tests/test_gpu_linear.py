@@ -566,19 +566,18 @@ def product(s, cout):
     return torch.cat([x @ w[n:n + 1024].t() for n in range(0, cout, 1024)], 1)
 
 
-# rows, out_features: a cluster for each tile; one CTA for each; pairs of CTAs
-KERNELS = [(3, 512), (40, 148 * 512), (512, 2048)]
+# rows, out_features: a cluster for each tile; one CTA for each; a cluster for 128 rows; pairs of CTAs
+KERNELS = [(3, 512), (40, 148 * 512), (512, 2048), (2048, 2048)]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 @pytest.mark.parametrize("rows,cout", KERNELS)
 def test_exactness_of_deep_sums(ep, kind, rows, cout):
-    """fp32 outputs of 7168 channels. Tensor memory cuts about 1.5e-8 of a sum
-    with each step of 16 channels. bf16: 32 steps at a time (4.8e-7 in the mean,
-    under 1e-6 with their spread), then 14 parts and at most 8 of a cluster are
-    added in fp32 (2^-24 each at most, of either sign: under 1e-6). All 448 steps
-    in one go would cut 6.7e-6. e4m3: 56 blocks of 4 steps, each scaled and added
-    in fp32, with 72 roundings of 2^-24 at most."""
+    """fp32 outputs of 7168 channels. Tensor memory cuts its sums. bf16: 32
+    steps of 16 channels at a time (8e-7 in the mean, with little spread), then 14
+    parts and at most 8 of a cluster are added in fp32 (2^-24 each at most, of
+    either sign: under 1e-6). All 448 steps in one go cut 2.7e-5. e4m3: 56 blocks
+    of 4 steps, each scaled and added in fp32, with 72 roundings of 2^-24 at most."""
     s = positive(1, kind, rows, 7168, cout)
     o = torch.empty(rows, cout, device=DEV)
     ep.ep_linear(buffer(ep, 1, 1, 1, 1), s["x"], s["w"], o, x_scale=s["x_scale"], w_scale=s["w_scale"])
@@ -586,13 +585,12 @@ def test_exactness_of_deep_sums(ep, kind, rows, cout):
     ref.within(o, y, y * (2e-6 if kind == "bf16" else 72 * 2.0 ** -24), "out")
 
 
-@pytest.mark.parametrize("rows,cout", [(3, 128), (300, 256)])
-def test_bf16_outputs_of_the_deepest_sums(ep, rows, cout):
-    """2^19 channels, bf16 out: half a step of the value itself, and what the
-    sum may lose: 512 steps in tensor memory (7.7e-6), 64 parts added in fp32
-    (3.8e-6). In one go it would be cut by 5e-4, and every tenth output would be
-    rounded the wrong way."""
-    cin = 2 ** 19
+@pytest.mark.parametrize("rows,cout,cin", [(3, 128, 2 ** 19), (300, 256, 2 ** 19), (4096, 2048, 2 ** 15)])
+def test_bf16_outputs_of_the_deepest_sums(ep, rows, cout, cin):
+    """bf16 out: half a step of the value itself, and what the sum may lose:
+    128 steps in tensor memory (5e-6), 256 parts added in fp32 (2^-24 each at
+    most). In one go 2^15 channels lose 1.7e-4, and one output in 30 is rounded
+    the wrong way."""
     s = positive(1, "bf16", rows, cin, cout)
     o = torch.empty(rows, cout, dtype=BF, device=DEV)
     ep.ep_linear(buffer(ep, 1, 1, 1, 1), s["x"], s["w"], o)
