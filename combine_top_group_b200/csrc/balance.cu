@@ -24,7 +24,7 @@
 
 #include "common.cuh"
 #include "ep.h"
-#include "fail.h"
+#include "block.h"
 #include "internal.h"
 
 namespace ep {

@@ -11,7 +11,7 @@
 #include <new>
 
 #include "ep.h"
-#include "fail.h"
+#include "block.h"
 #include "internal.h"
 
 namespace {
@@ -599,6 +599,7 @@ ep_status_t ep_selftest_wait_timeout(uint32_t* d_words, uint64_t limit_ns, uint3
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = ep::launch_barrier_timeout_selftest(d_words, limit_ns, s);
     if (e == cudaSuccess) e = ep::launch_mbarrier_timeout_selftest(d_words + 2, d_words + 3, limit_ns, s);
+    if (e == cudaSuccess) e = ep::launch_linear_timeout_selftest(d_words + 2, d_words, limit_ns, s);
     uint32_t v = 0;
     if (e == cudaSuccess) e = cudaMemcpyAsync(&v, d_words + 2, sizeof v, cudaMemcpyDeviceToHost, s);
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);

@@ -29,7 +29,7 @@
 #include <atomic>
 
 #include "ep.h"
-#include "fail.h"
+#include "block.h"
 #include "internal.h"
 #include "linear.cuh"
 
@@ -37,6 +37,29 @@ namespace ep {
 namespace {
 
 using namespace linear;
+
+// Self-test of the bounded waits: a barrier that expects one arrival nobody
+// makes. Warp 0 gives up after the limit; warp 1, whose own limit is far off,
+// follows its stop flag; then warp 0 drains. No copy or product is in flight.
+__global__ void timeout_selftest_kernel(uint32_t* err, uint32_t* gave_up, long long limit) {
+    __shared__ uint64_t bar;
+    __shared__ uint32_t stop;
+    const uint32_t at = tc::smem_u32(&bar);
+    if (threadIdx.x == 0) {
+        tc::bar_init(at, 1);
+        stop = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    const bool met = threadIdx.x < 32 ? tc::bar_wait<tc::kCluster>(at, 0, &stop, limit)
+                                      : tc::bar_wait(at, 0, &stop, tc::kWaitLimitCycles);
+    if (threadIdx.x < 32) tc::bar_drain(at, 0, clock64(), limit / 4);
+    const bool any_met = __syncthreads_or(met);
+    if (threadIdx.x == 0 && !any_met && stop) {
+        *gave_up = 1u;
+        set_error(err, EP_DEVERR_TIMEOUT);
+    }
+}
 
 // ---- host ----------------------------------------------------------------------
 
@@ -298,6 +321,15 @@ ep_status_t launch(const ep_buffer& b, const LinearParams& p, int64_t x_rows, in
 }
 
 }  // namespace
+
+cudaError_t launch_linear_timeout_selftest(uint32_t* err, uint32_t* gave_up, unsigned long long limit_ns,
+                                           cudaStream_t stream) {
+    cudaError_t e = cudaMemsetAsync(gave_up, 0, sizeof(uint32_t), stream);
+    if (e != cudaSuccess) return e;
+    timeout_selftest_kernel<<<1, 64, 0, stream>>>(err, gave_up, 2 * (long long)limit_ns);  // 2 cycles a nanosecond
+    return cudaGetLastError();
+}
+
 }  // namespace ep
 
 extern "C" {

@@ -72,13 +72,14 @@ constexpr long long kWaitLimitCycles = 4000000000ll;
 // Waits for the phase with this parity; false after the limit, or once
 // another thread of the CTA has given up (*stop).
 template <Scope SCOPE = kCta>
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* stop) {
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* stop,
+                                         long long limit = kWaitLimitCycles) {
     if (bar_try<SCOPE>(bar, parity)) return true;
     const long long t0 = clock64();
     while (!bar_try<SCOPE>(bar, parity)) {
         if (*stop) return false;
         __nanosleep(20);  // leaves the issue slots to the warps at work (e4m3 SwiGLU layer: 422 -> 397 us)
-        if (clock64() - t0 > kWaitLimitCycles) {
+        if (clock64() - t0 > limit) {
             *stop = 1;
             return false;
         }
@@ -87,9 +88,9 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
 }
 // The same without the stop flag, for draining what a stopped CTA has in
 // flight; several drains share the limit from t0 on.
-__device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity, long long t0) {
+__device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity, long long t0, long long limit = kWaitLimitCycles) {
     while (!bar_try(bar, parity))
-        if (clock64() - t0 > kWaitLimitCycles) return;
+        if (clock64() - t0 > limit) return;
 }
 // About 1 ms, a thousand times what a store into another CTA's shared memory takes.
 constexpr long long kPushCycles = 2000000ll;

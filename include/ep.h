@@ -559,7 +559,10 @@ ep_status_t ep_expert_linear(ep_buffer_t *buf, int T, const ep_linear_t *p, void
  *    reached: every CTA must give up and set EP_DEVERR_TIMEOUT;
  *  - the capped combine pipeline's mbarrier wait on a phase that never
  *    completes: it must give up, set EP_DEVERR_TIMEOUT and write 1 to
- *    d_words[3].
+ *    d_words[3];
+ *  - the linear layers' waits on a phase that never completes, and a drain
+ *    after them (limit_ns at 2 cycles a nanosecond): each must end, set
+ *    EP_DEVERR_TIMEOUT and write 1 to d_words[0].
  * d_words: 4 device uint32 of scratch, owned by the caller. The call
  * synchronises `stream` and returns the error bits in *word. It never traps,
  * and the CUDA context stays usable. (The pages have no counterpart: it checks

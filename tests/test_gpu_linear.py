@@ -597,3 +597,17 @@ def test_bf16_outputs_of_the_deepest_sums(ep, rows, cout, cin):
     y = product(s, cout)
     half = torch.ldexp(torch.ones_like(y), torch.frexp(y).exponent - 9)
     ref.within(o, y, half + y * 2e-5, "out")
+
+
+def test_waits_give_up(ep):
+    """The kernels' waits end after their limit, or when another warp has given
+    up, and the next call on the same context works."""
+    import time
+    words = torch.zeros(4, dtype=torch.int32, device=DEV)
+    t0 = time.perf_counter()
+    bits = ep.ep_selftest_wait_timeout(words, 50_000_000)
+    assert bits & ep.EP_DEVERR_TIMEOUT
+    assert words[0] == 1 and words[3] == 1
+    # three waits of 50 ms; the linear layers' run on the SM's clock, up to 2 GHz; none took its full 2 s
+    assert 0.14 < time.perf_counter() - t0 < 1.5
+    dense(ep, "bf16", 70, 256, 300, 0, True, False, "bf16")
