@@ -294,7 +294,7 @@ ep_status_t launch_on_device(const ep_buffer& b, LinearParams p, int64_t x_rows,
     const int64_t tiles = bound * p.nt, pairs = b.sm_count / 2, clusters = split ? clusters_of(b, p.splits) : 0;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(pair ? 2 * (tiles < pairs ? tiles : pairs) : split ? p.splits * (tiles < clusters ? tiles : clusters) : tiles < b.sm_count ? tiles : b.sm_count));
-    cfg.blockDim = dim3(pair ? kThreads : kThreads);
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = pair ? kPairSmem : smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

@@ -34,7 +34,7 @@ struct LinearParams {
     int64_t row_limit;     // rows the arrays hold
     uint32_t* err;
     // shape of the launch
-    int bn;        // rows of x per tile: 32, 64 or 128
+    int bn;        // rows of x per tile: 32, 64 or 128; 256 with pairs of CTAs
     int na;        // 128-channel weight tiles per CTA tile: gate and up, or neighbours
     int nt;        // channel tiles: out_features over 128 (swiglu) or 128 * na
     int stages;    // of the shared-memory ring

@@ -511,8 +511,11 @@ typedef enum {
  *    multiple of 128 and out_scale fp32 [rows, out_features/128]: the cast of
  *    ep_dispatch, from fp32. Otherwise out_scale is NULL.
  * Products of bf16 or e4m3 values are exact and summed in fp32 (e4m3: per 128
- * channels, then scaled and summed); the epilogue is fp32 with one rounding at
- * the end. Rows are contiguous. x and w are 16-byte aligned, out and residual
+ * channels, then scaled and summed; bf16: in tensor memory, which cuts instead
+ * of rounding: operands of one sign are off by 8e-7 for fp32 and e4m3 out, by up
+ * to 3.2e-5 for bf16 out); the epilogue is fp32 with one rounding at the end.
+ * EP_ACT_GELU takes 1 + erf(z / sqrt 2) in fp32, so where z is negative it is
+ * off by up to 1e-7 |z|; the sigmoids are off by up to 1e-5 of themselves. Rows are contiguous. x and w are 16-byte aligned, out and residual
  * 16-byte, scales and bias 4-byte. out may be residual itself where out_type
  * is EP_DTYPE_BF16. */
 typedef struct {
@@ -532,7 +535,9 @@ typedef struct {
 
 /* Dense layer on `rows` rows: the router projection (fp32 out, which
  * ep_get_layout takes as logits), a shared expert. buf gives the device and
- * the error word; its layout is not used.
+ * the error word; its layout is not used. The buffer's SM budget
+ * (ep_buffer_set_num_sms) is that of dispatch and combine: this call and
+ * ep_expert_linear run on every SM that is free.
  * Errors: EP_ERR_INVALID, EP_ERR_UNSUPPORTED. */
 ep_status_t ep_linear(ep_buffer_t *buf, int64_t rows, const ep_linear_t *p, void *stream);
 
