@@ -300,6 +300,11 @@ __device__ __forceinline__ bool epi_sync_and(bool ok) {
         : "memory");
     return r != 0;
 }
+// Every warp of the CTA is through with its tiles: from here on the stop flag
+// is final. (A barrier of its own, as the warps come to it from two branches:
+// with one after both, what drains needs stayed in the epilogue's registers, and
+// an e4m3 layer of 4096 x 8192 -> 8192 took 406 us instead of 394.)
+__device__ __forceinline__ void all_done() { asm volatile("bar.sync 6, %0;" ::"n"(kThreads) : "memory"); }
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory"); }
 
 // Pairs of CTAs.

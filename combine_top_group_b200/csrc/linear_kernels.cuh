@@ -78,13 +78,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kElems = F8 ? 128 : 64;  // in_features of a block
     Cursor cur;
     Tile t;
-    int loads = 0;  // that the loads warp has issued
 
     // The loads and products warps run their loops whole and converged; one
     // elected lane issues. A warpgroup changes its registers by one instruction
     // that all its warps execute, before they part.
     if (warp >= kEpiWarps) {
         tc::fewer_registers<kOtherRegs>();
+        int loads = 0;  // that the loads warp has issued
         if (warp == kEpiWarps) {  // loads
             int s = 0;
             uint32_t wrap = 0;
@@ -205,6 +205,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
+        __syncwarp();
+        all_done();
+        // A wait gave up: copies and products in flight end before the CTA leaves.
+        // (Otherwise the epilogue has waited for them all.)
+        if (*stop) {
+            const long long t0 = clock64();
+            if (warp == kEpiWarps) {
+                for (int j = max(loads - stages, 0); j < loads; ++j) tc::bar_drain(full(j % stages), (j / stages) & 1, t0);
+            } else if (warp == kEpiWarps + 1) {
+                if (tc::elect()) tc::commit(drained);
+                tc::bar_drain(drained, 0, t0);
+            }
+            __syncwarp();
+        }
     } else {  // epilogue: warps 0-3 read sub-tile 0, warps 4-7 sub-tile 1
         tc::more_registers<kEpiRegs>();
         const int sub = warp >> 2;
@@ -324,21 +338,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
+        __syncwarp();
+        all_done();
     }
     __syncwarp();
-    __syncthreads();
-    // A wait gave up: copies and products in flight end before the CTA leaves.
-    // (Otherwise the epilogue has waited for them all.)
-    if (*stop) {
-        const long long t0 = clock64();
-        if (warp == kEpiWarps) {
-            for (int j = max(loads - stages, 0); j < loads; ++j) tc::bar_drain(full(j % stages), (j / stages) & 1, t0);
-        } else if (warp == kEpiWarps + 1) {
-            if (tc::elect()) tc::commit(drained);
-            tc::bar_drain(drained, 0, t0);
-        }
-        __syncwarp();
-    }
     if (SPLIT) {
         tc::cluster_sync();  // no CTA leaves while another may push into its inbox
         // pushes issued before that into an inbox that nobody waits for any more
@@ -481,10 +484,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     constexpr int kElems = F8 ? 128 : 64;
     Cursor cur;
     Tile t;
-    int loads = 0;  // that the loads warp has issued
 
     if (warp >= kEpiWarps) {
         tc::fewer_registers<kPairOtherRegs>();
+        int loads = 0;  // that the loads warp has issued
         if (warp == kEpiWarps) {  // loads, each CTA its halves
             int s = 0;
             uint32_t wrap = 0;
@@ -545,6 +548,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                 }
             }
+        }
+        __syncwarp();
+        all_done();
+        // A wait gave up: the pair's copies and products in flight end before it
+        // leaves. The leader's barriers count both CTAs' copies, and a leader that no
+        // wait stopped has seen them all land.
+        if (*stop && rank == 0) {
+            const long long t0 = clock64();
+            if (warp == kEpiWarps) {
+                for (int j = max(loads - kPairStages, 0); j < loads; ++j)
+                    tc::bar_drain(full(j % kPairStages), (j / kPairStages) & 1, t0);
+            } else if (warp == kEpiWarps + 1) {
+                if (tc::elect()) tc::pair_commit(drained);
+                tc::bar_drain(drained, 0, t0);
+            }
+            __syncwarp();
         }
     } else {  // epilogue: warps w and w + 4 share 32 rows, half of the channels each
         tc::more_registers<kPairEpiRegs>();
@@ -724,23 +743,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 ++acc;
             }
         }
+        __syncwarp();
+        all_done();
     }
     __syncwarp();
-    __syncthreads();
-    // A wait gave up: the pair's copies and products in flight end before it
-    // leaves. The leader's barriers count both CTAs' copies, and a leader that no
-    // wait stopped has seen them all land.
-    if (*stop && rank == 0) {
-        const long long t0 = clock64();
-        if (warp == kEpiWarps) {
-            for (int j = max(loads - kPairStages, 0); j < loads; ++j)
-                tc::bar_drain(full(j % kPairStages), (j / kPairStages) & 1, t0);
-        } else if (warp == kEpiWarps + 1) {
-            if (tc::elect()) tc::pair_commit(drained);
-            tc::bar_drain(drained, 0, t0);
-        }
-        __syncwarp();
-    }
     tc::cluster_sync();
     if (threadIdx.x == 0 && *stop) set_error(p.err, EP_DEVERR_TIMEOUT);
     if (warp == kEpiWarps + 1) tc::pair_tmem_free(tmem, 512);

@@ -63,12 +63,14 @@ def test_a_stopped_cta_drains_whatever_stopped_it(name):
     after the barrier of the whole CTA, where the stop flag is final, and not
     by the one warp that saw its own wait fail."""
     k = kernels()[name]
-    end = k.rindex("__syncthreads();")
+    assert k.count("all_done();") == 2  # the epilogue's and the other warps' arrival at one barrier
+    end = k.index("all_done();")
     assert "bar_drain" not in k[:end]
     after = k[end:]
-    assert re.match(r"__syncthreads\(\); if \(\*stop( && rank == 0)?\) \{", after)
+    assert re.match(r"all_done\(\); if \(\*stop( && rank == 0)?\) \{", after)
     assert re.search(r"bar_drain\(full\(", after) and re.search(r"commit\(drained\); tc::bar_drain\(drained", after)
-    assert after.index("bar_drain") < after.index("cluster_sync") < after.index("tmem_free")
+    assert after.rindex("bar_drain") < after.rindex("all_done();") < after.rindex("cluster_sync") < after.index("tmem_free")
+    assert re.search(r'all_done\(\) \{ asm volatile\("bar.sync 6, %0;" ::"n"\(kThreads\)', code("linear.cuh"))
 
 
 def test_an_unfilled_inbox_is_not_armed_again():
