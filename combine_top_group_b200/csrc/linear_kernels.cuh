@@ -11,8 +11,9 @@ namespace linear {
 namespace {
 
 // Output channels as lanes, rows of x as columns, one CTA or a cluster to a
-// tile: for few rows. 32 experts of 32 rows, 7168 -> 2 x 2048, e4m3: 161 us,
-// 5.9 TB/s of weights (90% of a copy's rate). BN: rows of x per tile (p.bn).
+// tile: for few rows. 32 experts of 32 rows, 7168 -> 2 x 2048, e4m3: 184 to 196
+// us under the power cap (1.64 GHz), 4.8 to 5.2 TB/s (74 to 79% of a copy's
+// rate). BN: rows of x per tile (p.bn).
 template <bool F8, bool SPLIT, int BN>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, LinearParams p) {
@@ -361,8 +362,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // read for two products of 128 x 128; shared memory is what bounds those. A
 // thread owns a row: its e4m3 scale is one register, and the epilogue needs no
 // exchange but the amax of an e4m3 row between two warps. 4096 x 8192 -> 8192
-// in bf16: 1.45 PFLOP/s (90% of a cuBLAS burst), tensor cores 96% busy while
-// active; in e4m3 1.6 PFLOP/s, bound by the hand-over of each block's sums.
+// in bf16: 371 us in a burst (1.48 PFLOP/s, 92% of a cuBLAS burst), 444 under the
+// power cap (1.26 GHz), tensor cores 92% busy while active; in e4m3 394 us (1.40
+// PFLOP/s, no faster), bound by the hand-over of each block's sums.
 
 
 // 16 channels of a row at n, rounded and stored in 16-byte pieces. (A lane
