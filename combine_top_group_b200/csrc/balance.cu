@@ -22,9 +22,9 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "block.h"
 #include "common.cuh"
 #include "ep.h"
-#include "block.h"
 #include "internal.h"
 
 namespace ep {

@@ -10,8 +10,8 @@
 
 #include <new>
 
-#include "ep.h"
 #include "block.h"
+#include "ep.h"
 #include "internal.h"
 
 namespace {

@@ -28,8 +28,8 @@
 
 #include <atomic>
 
-#include "ep.h"
 #include "block.h"
+#include "ep.h"
 #include "internal.h"
 #include "linear.cuh"
 

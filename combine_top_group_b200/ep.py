@@ -352,8 +352,8 @@ def ep_combine_dedup(buf: EpBuffer, T: int, out, stream=None) -> None:
 
 
 def ep_selftest_wait_timeout(words, limit_ns: int, stream=None) -> int:
-    """Runs a bounded wait that can never be satisfied; returns the error
-    bits it left (EP_DEVERR_TIMEOUT expected). `words`: 4-element int32/uint32
+    """Runs bounded waits that can never be satisfied; returns the error
+    bits they left (EP_DEVERR_TIMEOUT expected). `words`: 4-element int32/uint32
     CUDA tensor."""
     w = ctypes.c_uint32(0)
     _check(_lib.ep_selftest_wait_timeout(_ptr(words), limit_ns, ctypes.byref(w), _stream(stream)),
