@@ -515,9 +515,10 @@ typedef enum {
  * of rounding: operands of one sign are off by 8e-7 for fp32 and e4m3 out, by up
  * to 3.2e-5 for bf16 out); the epilogue is fp32 with one rounding at the end.
  * EP_ACT_GELU takes 1 + erf(z / sqrt 2) in fp32, so where z is negative it is
- * off by up to 1e-7 |z|; the sigmoids are off by up to 1.3e-5 of themselves. Rows are contiguous. x and w are 16-byte aligned, out and residual
- * 16-byte, scales and bias 4-byte. out may be residual itself where out_type
- * is EP_DTYPE_BF16. */
+ * off by up to 1e-7 |z|; the sigmoids are off by up to 1.3e-5 of themselves.
+ * Rows are contiguous. x and w are 16-byte aligned, out and residual 16-byte,
+ * scales and bias 4-byte. out may be residual itself where out_type is
+ * EP_DTYPE_BF16. */
 typedef struct {
     const void *x;
     const float *x_scale;
